@@ -73,6 +73,8 @@ typedef enum {
 
 /* Bits of the device status word (w4a4_get_device_status). */
 #define W4A4_DEV_TIMEOUT 0x1u
+#define W4A4_DEV_RANGE 0x2u   /* a position, length, sequence or page number read on the
+                                 device was out of range (decode.h) */
 
 /* Flags. */
 #define W4A4_FLAG_GELU  0x1u  /* quantize_act / linear_fused: apply exact-erf GELU
@@ -368,7 +370,8 @@ w4a4_status w4a4_gemm_s32_ex(const uint8_t *qx, int64_t M, const w4a4_weights_t 
 
 /* Synchronizes `stream`, then copies the device status word (bits
  * W4A4_DEV_*) of the current device into *status.  Returns W4A4_ERR_TIMEOUT
- * when a bit is set, W4A4_OK otherwise. */
+ * when W4A4_DEV_TIMEOUT is set, W4A4_ERR_ARG when only W4A4_DEV_RANGE is,
+ * W4A4_OK otherwise. */
 w4a4_status w4a4_get_device_status(void *stream, uint32_t *status);
 
 /* Clears the device status word of the current device (enqueued on stream). */

@@ -316,7 +316,8 @@ w4a4_status w4a4_get_device_status(void *stream, uint32_t *status) {
   cudaError_t e = w4a4::read_status(&v, as_stream(stream));
   if (e != cudaSuccess) return W4A4_ERR_CUDA;
   *status = v;
-  return v ? W4A4_ERR_TIMEOUT : W4A4_OK;
+  if (v & W4A4_DEV_TIMEOUT) return W4A4_ERR_TIMEOUT;
+  return v ? W4A4_ERR_ARG : W4A4_OK;
 }
 
 w4a4_status w4a4_clear_device_status(void *stream) {

@@ -1,4 +1,4 @@
-"""ctypes binding of libw4a4 (include/w4a4.h) for torch tensors.
+"""ctypes binding of libw4a4 (include/w4a4.h, tq.h, decode.h) for torch tensors.
 
 Argument marshalling only: every step of the computation runs in the CUDA
 library.  Importing this module raises ImportError when libw4a4.so has not
@@ -11,6 +11,7 @@ Calls are asynchronous on the given stream (default: torch's current stream).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -25,6 +26,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 W4A4_OK, W4A4_ERR_ARG, W4A4_ERR_SHAPE, W4A4_ERR_ALIGN, W4A4_ERR_UNSUPPORTED, W4A4_ERR_CUDA, \
     W4A4_ERR_TIMEOUT = range(7)
 W4A4_DEV_TIMEOUT = 0x1
+W4A4_DEV_RANGE = 0x2
 W4A4_FLAG_GELU = 0x1
 W4A4_FLAG_PLAIN = 0x2
 W4A4_FLAG_INT8 = 0x4
@@ -32,6 +34,8 @@ W4A4_FLAG_UNPACKED = 0x8
 W4A4_FLAG_GELU_OUT = 0x10
 W4A4_FLAG_X_DEVICE = 0x20
 W4A4_FLAG_FWHT = 0x100
+W4A4_FLAG_FP16 = 0x200
+W4A4_FLAG_ROPE_PAIRS = 0x400
 W4A4_FLAG_Y_DEVICE = 0x40
 W4A4_DEBUG_STALL = 0x80000000
 
@@ -42,6 +46,16 @@ _vp, _i32, _i64, _u32, _f32, _sz = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_in
 class W4A4WeightsT(ctypes.Structure):
     _fields_ = [("N", _i32), ("K", _i32), ("qw", _vp), ("scale_ch", _vp), ("bias", _vp),
                 ("smooth", _vp), ("inv_smooth", _vp), ("qw8", _vp), ("colsum", _vp), ("flags", _u32)]
+
+
+class GroupWeightsT(ctypes.Structure):
+    _fields_ = [("N", _i32), ("K", _i32), ("group", _i32), ("flags", _u32), ("codes", _vp), ("scales", _vp)]
+
+
+class KVCacheT(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("n_pages", _i64), ("page_size", _i32), ("n_heads", _i32),
+                ("head_dim", _i32), ("flags", _u32), ("stride_page", _i64), ("stride_token", _i64),
+                ("stride_head", _i64)]
 
 
 def _sig(name, res, args):
@@ -83,6 +97,22 @@ _tq_decode = _sig("tq_decode", ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _v
 _tq_rotation_qr = _sig("tq_rotation_qr", ctypes.c_int, [_vp, _i32, _vp, _vp, _vp, _vp])
 _tq_encode_dense = _sig("tq_encode_dense", ctypes.c_int, [_vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp])
 _tq_decode_dense = _sig("tq_decode_dense", ctypes.c_int, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp])
+_group_bytes = _sig("w4a4_group_weights_bytes", _sz, [_i32, _i32, _i32])
+_group_bind = _sig("w4a4_group_bind", ctypes.c_int,
+                   [_vp, _sz, _i32, _i32, _i32, _u32, ctypes.POINTER(GroupWeightsT)])
+_group_quantize = _sig("w4a4_group_quantize", ctypes.c_int, [_vp, ctypes.POINTER(GroupWeightsT), _vp])
+_group_pack = _sig("w4a4_group_pack", ctypes.c_int, [_vp, _vp, ctypes.POINTER(GroupWeightsT), _vp])
+_group_dequantize = _sig("w4a4_group_dequantize", ctypes.c_int, [ctypes.POINTER(GroupWeightsT), _vp, _vp])
+_group_gemv = _sig("w4a4_group_gemv", ctypes.c_int,
+                   [_vp, _i64, ctypes.POINTER(GroupWeightsT), _vp, _vp, _u32, _vp])
+_rope_table = _sig("w4a4_rope_table", ctypes.c_int, [_i32, _i32, ctypes.c_double, _vp])
+_kv_append = _sig("w4a4_kv_append", ctypes.c_int,
+                  [ctypes.POINTER(KVCacheT), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32,
+                   _vp, _vp, _vp, _i32, _i32, _vp, _u32, _vp])
+_kv_attend_ws = _sig("w4a4_kv_attend_workspace_bytes", _sz, [_i32, _i32, _i32, _i32])
+_kv_attend = _sig("w4a4_kv_attend", ctypes.c_int,
+                  [_vp, _i64, _i32, ctypes.POINTER(KVCacheT), _vp, _i32, _i32, _vp, _f32, _i32, _vp, _vp, _vp,
+                   _sz, _vp])
 _status_string = _sig("w4a4_status_string", ctypes.c_char_p, [ctypes.c_int])
 _version = _sig("w4a4_version", ctypes.c_char_p, [])
 
@@ -306,7 +336,7 @@ def w4a4_gemm_s32_ex(qx: torch.Tensor, w: PreparedWeights, flags: int = 0, acc=N
 def w4a4_get_device_status(stream=None) -> int:
     v = _u32(0)
     rc = _get_status(_stream(stream), ctypes.byref(v))
-    if rc not in (W4A4_OK, W4A4_ERR_TIMEOUT):
+    if not (rc in (W4A4_OK, W4A4_ERR_TIMEOUT) or (rc == W4A4_ERR_ARG and v.value)):
         _check(rc, "w4a4_get_device_status")
     return int(v.value)
 
@@ -379,3 +409,224 @@ def tq_decode_dense(codes: torch.Tensor, norms: torch.Tensor, pit_hi: torch.Tens
     _check(_tq_decode_dense(_ptr(codes), _ptr(norms), n, d, _ptr(pit_hi), _ptr(pit_lo), _ptr(centroids),
                             _ptr(Y), _stream(stream)), "tq_decode_dense")
     return Y
+
+
+# ------------------------------------------- single-token operators (include/decode.h)
+def _enter(dev: torch.device, stream):
+    """The stream to launch on, and a context that makes `dev` current (and
+    `stream` the allocating one) where it is not; None when nothing has to change."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.current_stream(dev).cuda_stream, torch.cuda.device(dev)
+    return torch.cuda.current_stream().cuda_stream, None
+
+
+def _need(t: torch.Tensor, name: str, dtype, dev, shape) -> int:
+    """The address of a contiguous tensor of that type, device and shape."""
+    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, name: str, dtype, dev, shape) -> tuple[int, int]:
+    """Address and row stride of a tensor [T, heads, head_dim] whose rows are dense."""
+    if t.dtype != dtype or t.device != dev or t.shape != shape:
+        raise ValueError(f"{name}: need {dtype} of shape {tuple(shape)} on {dev}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    T, H, D = shape
+    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, strides are {t.stride()}")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def _half_flag(dtype) -> int:
+    if dtype == torch.bfloat16:
+        return 0
+    if dtype == torch.float16:
+        return W4A4_FLAG_FP16
+    raise ValueError(f"need torch.bfloat16 or torch.float16, got {dtype}")
+
+
+def _cuda_device(t: torch.Tensor, name: str) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.device
+
+
+def w4a4_group_weights_bytes(N: int, K: int, group: int) -> int:
+    return int(_group_bytes(N, K, group))
+
+
+class GroupWeights:
+    """4-bit weights [N, K] with one step per `group` inputs: one torch-owned
+    allocation of w4a4_group_weights_bytes(N, K, group) bytes, laid out by
+    w4a4_group_bind, to be filled by w4a4_group_quantize or w4a4_group_pack.
+    dtype: of the steps and of the tokens they multiply."""
+
+    def __init__(self, N: int, K: int, group: int = 128, dtype=torch.bfloat16, device="cuda"):
+        self.N, self.K, self.group, self.dtype = N, K, group, dtype
+        flags = _half_flag(dtype)
+        nbytes = w4a4_group_weights_bytes(N, K, group)
+        if nbytes == 0:
+            raise W4A4Error(W4A4_ERR_UNSUPPORTED if group not in (32, 64, 128) else W4A4_ERR_SHAPE,
+                            "w4a4_group_weights_bytes")
+        self.storage = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.device = self.storage.device
+        self.struct = GroupWeightsT()
+        _check(_group_bind(_ptr(self.storage), nbytes, N, K, group, flags, ctypes.byref(self.struct)),
+               "w4a4_group_bind")
+
+
+def w4a4_group_quantize(W: torch.Tensor, group: int = 128, out: GroupWeights | None = None,
+                        stream=None) -> GroupWeights:
+    """W [N, K] bf16 or fp16 -> 4-bit codes with one step per `group` inputs."""
+    dev = _cuda_device(W, "W")
+    N, K = W.shape
+    st, ctx = _enter(dev, stream)
+    with ctx or contextlib.nullcontext():
+        out = out if out is not None else GroupWeights(N, K, group, W.dtype, dev)
+        if out.group != group or out.device != dev:
+            raise ValueError(f"out has groups of {out.group} on {out.device}, asked for {group} on {dev}")
+        w = _need(W, "W", out.dtype, dev, (out.N, out.K))
+        _check(_group_quantize(w, ctypes.byref(out.struct), st), "w4a4_group_quantize")
+    return out
+
+
+def w4a4_group_pack(codes: torch.Tensor, scales: torch.Tensor, out: GroupWeights | None = None,
+                    stream=None) -> GroupWeights:
+    """codes [N, K/2] uint8 (element 2i in the low nibble) and scales [N,
+    K/group] made elsewhere -> GroupWeights."""
+    dev = _cuda_device(codes, "codes")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    st, ctx = _enter(dev, stream)
+    with ctx or contextlib.nullcontext():
+        if out is None:
+            if scales.dim() != 2 or scales.shape[1] == 0 or K % scales.shape[1]:
+                raise ValueError(f"scales {tuple(scales.shape)} do not divide {K} inputs into groups")
+            out = GroupWeights(N, K, K // scales.shape[1], scales.dtype, dev)
+        c = _need(codes, "codes", torch.uint8, out.device, (out.N, out.K // 2))
+        s = _need(scales, "scales", out.dtype, out.device, (out.N, out.K // out.group))
+        _check(_group_pack(c, s, ctypes.byref(out.struct), st), "w4a4_group_pack")
+    return out
+
+
+def w4a4_group_dequantize(w: GroupWeights, W=None, stream=None) -> torch.Tensor:
+    """The weights [N, K] that the codes and steps stand for."""
+    st, ctx = _enter(w.device, stream)
+    with ctx or contextlib.nullcontext():
+        W = W if W is not None else torch.empty((w.N, w.K), dtype=w.dtype, device=w.device)
+        p = _need(W, "W", w.dtype, w.device, (w.N, w.K))
+        _check(_group_dequantize(ctypes.byref(w.struct), p, st), "w4a4_group_dequantize")
+    return W
+
+
+def w4a4_group_gemv(X: torch.Tensor, w: GroupWeights, bias=None, Y=None, flags: int = 0,
+                    stream=None) -> torch.Tensor:
+    """Y [M, N] = X [M, K] W^T + bias for up to 16 tokens."""
+    M = X.shape[0]
+    st, ctx = _enter(w.device, stream)
+    with ctx or contextlib.nullcontext():
+        x = _need(X, "X", w.dtype, w.device, (M, w.K))
+        b = None if bias is None else _need(bias, "bias", w.dtype, w.device, (w.N,))
+        Y = Y if Y is not None else torch.empty((M, w.N), dtype=w.dtype, device=w.device)
+        y = _need(Y, "Y", w.dtype, w.device, (M, w.N))
+        _check(_group_gemv(x, M, ctypes.byref(w.struct), b, y, flags, st), "w4a4_group_gemv")
+    return Y
+
+
+def w4a4_rope_table(n_pos: int, rot_dim: int, base: float = 10000.0):
+    """Host: the rotation table [n_pos, rot_dim] (numpy fp32), cos then sin per row."""
+    import numpy as np
+    table = np.empty((n_pos, rot_dim), np.float32)
+    _check(_rope_table(n_pos, rot_dim, base, table.ctypes.data_as(_vp)), "w4a4_rope_table")
+    return table
+
+
+class KVCache:
+    """Keys and values in pages: two tensors [n_pages, page_size, heads,
+    head_dim] of the same strides, the last dimension contiguous.  A pool kept
+    as [n_pages, heads, page_size, head_dim] is passed transposed(1, 2)."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor):
+        dev = _cuda_device(k, "k")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or v.device != dev or k.stride() != v.stride():
+            raise ValueError("k and v must be 4-dimensional and agree in shape, strides, type and device")
+        if k.stride(3) != 1:
+            raise ValueError(f"head_dim must be contiguous, strides are {k.stride()}")
+        self.k, self.v, self.device, self.dtype = k, v, dev, k.dtype
+        P, S, H, D = k.shape
+        self.n_heads, self.head_dim, self.page_size, self.n_pages = H, D, S, P
+        # a dimension of one element has no stride of its own
+        sp, ss, sh = (k.stride(i) if k.shape[i] > 1 else 0 for i in range(3))
+        self.struct = KVCacheT(k.data_ptr(), v.data_ptr(), P, S, H, D, _half_flag(k.dtype), sp, ss, sh)
+
+
+def w4a4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor, pos: torch.Tensor,
+                   q=None, q_out=None, table=None, table_pos=None, seq=None, flags: int = 0, stream=None):
+    """k, v [T, heads, head_dim] enter the cache at position pos [T] (int32; negative: left out) of sequence
+    seq [T] (default: token t is sequence t), whose pages are the row of pages [n_seqs, max_pages].  Keys, and
+    q [T, q_heads, head_dim], are rotated by row table_pos[t] (default pos[t]) of table [n, rot_dim] fp32.
+    Returns the rotated q (None without q)."""
+    T = k.shape[0]
+    dev, dt = cache.device, cache.dtype
+    st, ctx = _enter(dev, stream)
+    with ctx or contextlib.nullcontext():
+        kp, ks = _rows(k, "k", dt, dev, (T, cache.n_heads, cache.head_dim))
+        vp, vs = _rows(v, "v", dt, dev, (T, cache.n_heads, cache.head_dim))
+        qp = qs = op = None
+        hq = 0
+        if q is not None:
+            hq = q.shape[1]
+            qp, qs = _rows(q, "q", dt, dev, (T, hq, cache.head_dim))
+            q_out = q_out if q_out is not None else torch.empty((T, hq, cache.head_dim), dtype=dt, device=dev)
+            op = _need(q_out, "q_out", dt, dev, (T, hq, cache.head_dim))
+        n_seqs, max_pages = pages.shape
+        n_table = rot = 0
+        tp = None
+        if table is not None:
+            n_table, rot = table.shape
+            tp = _need(table, "table", torch.float32, dev, (n_table, rot))
+        if seq is None and T > n_seqs:
+            raise ValueError(f"{T} tokens for {n_seqs} sequences need seq")
+        _check(_kv_append(ctypes.byref(cache.struct), kp, ks, vp, vs, qp, qs or 0, hq, op, T,
+                          _need(pages, "pages", torch.int32, dev, (n_seqs, max_pages)), n_seqs, max_pages,
+                          None if seq is None else _need(seq, "seq", torch.int32, dev, (T,)),
+                          _need(pos, "pos", torch.int32, dev, (T,)), tp, n_table, rot,
+                          None if table_pos is None else _need(table_pos, "table_pos", torch.int32, dev, (T,)),
+                          flags, st), "w4a4_kv_append")
+    return None if q is None else q_out
+
+
+def w4a4_kv_attend_workspace_bytes(n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(_kv_attend_ws(n_seqs, n_q_heads, n_kv_heads, head_dim))
+
+
+def w4a4_kv_attend(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: torch.Tensor, scale=None,
+                   window: int = 0, out=None, lse=None, workspace=None, stream=None) -> torch.Tensor:
+    """One new token per sequence: q [n_seqs, q_heads, head_dim] against the lens [n_seqs] (int32) cached
+    tokens of its sequence, the last `window` of them where window > 0.  scale: 1 / sqrt(head_dim) by
+    default.  lse [n_seqs, q_heads] fp32 receives the logarithm of the sum of exponentials."""
+    B, Hq, D = q.shape
+    dev, dt = cache.device, cache.dtype
+    st, ctx = _enter(dev, stream)
+    with ctx or contextlib.nullcontext():
+        qp, qs = _rows(q, "q", dt, dev, (B, Hq, cache.head_dim))
+        max_pages = pages.shape[1]
+        out = out if out is not None else torch.empty((B, Hq, D), dtype=dt, device=dev)
+        need = w4a4_kv_attend_workspace_bytes(B, Hq, cache.n_heads, D)
+        if workspace is None:
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
+        _check(_kv_attend(qp, qs, Hq, ctypes.byref(cache.struct),
+                          _need(pages, "pages", torch.int32, dev, (B, max_pages)), B, max_pages,
+                          _need(lens, "lens", torch.int32, dev, (B,)), D ** -0.5 if scale is None else scale,
+                          window, _need(out, "out", dt, dev, (B, Hq, D)),
+                          None if lse is None else _need(lse, "lse", torch.float32, dev, (B, Hq)),
+                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
+               "w4a4_kv_attend")
+    return out
