@@ -23,6 +23,15 @@ struct Bf16 {
     return *reinterpret_cast<const uint32_t *>(&h);
   }
   static __device__ __forceinline__ uint16_t round(float a) { return __bfloat16_as_ushort(__float2bfloat16_rn(a)); }
+  // d (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums
+  static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
 };
 
 struct Fp16 {
@@ -34,6 +43,15 @@ struct Fp16 {
     return *reinterpret_cast<const uint32_t *>(&h);
   }
   static __device__ __forceinline__ uint16_t round(float a) { return __half_as_ushort(__float2half_rn(a)); }
+  // d (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums
+  static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  }
 };
 
 inline bool ptr_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdint>
 
+#include "ctxcache.h"
 #include "decode.cuh"
 #include "decode.h"
 #include "kernels.h"
@@ -78,81 +79,494 @@ __global__ void __launch_bounds__(128) kv_append_kernel(AppendArgs a, unsigned i
   }
 }
 
+// ------------------------------------------------------------------- attend
+//
+// out[b, h] = sum_t p_t V[t], p = softmax_t(scale q.K[t]).  Every cached token
+// is read once, 4 D bytes per cache head, and used for 4 D flops per query head
+// that shares it: bound by HBM for any usual number of shared heads, so the
+// design is about keeping reads in flight.
+//
+//  * The work is the concatenation, over sequences, cache heads and chunks of up
+//    to 16 of the heads that share one, of tiles of 64 tokens.  The lengths are on
+//    the device, so every block of a grid that fills the GPU once adds them up
+//    and takes an equal share of that line: a long sequence is split over
+//    as many blocks as it needs, short ones share a block.  A block finishes
+//    the items that lie inside its share; of an item that it shares with other
+//    blocks it leaves maximum, sum and unnormalised output in the workspace
+//    (two at most: its first and its last), and kv_join_kernel joins those.
+//  * A warp works alone on 16 tokens at a time, through its own ring of
+//    stages filled by 16-byte asynchronous copies: no block-wide wait inside an
+//    item, and rows are addressed one by one, so pages may have any size.  Rows
+//    without a token are filled with zeros by the copy itself.
+//  * The products are m16n8k16 tensor-core instructions (a tile has at most 16
+//    rows of queries, so tcgen05's 128-row tiles would be nearly empty, and at
+//    HBM's pace these take a quarter of the tensor pipe).  Scores: A = queries (heads
+//    x dims), B = keys.  Its accumulator holds for head lane / 4 two neighbouring
+//    tokens per register pair, which is the B operand (tokens x heads) of the second
+//    product with A = V^T (dims x tokens): the weights never leave their lane.
+//    The order of dims inside a product is free as long as both operands share it,
+//    so a lane's operands are 16-byte pieces of rows as they lie in memory.
+//  * Weights enter the second product as two 16-bit terms (hi + lo, 2^-16 or
+//    better): one term would put an error of half a bf16 step on every weight,
+//    as large as the rounding of the result.
+
+constexpr int kAttendWarps = 4;
+constexpr int kTile = 64;            // tokens of a block's tile: 16 per warp
+constexpr int kMaxBlocks = 640;      // partial results in the workspace: 2 per block
+constexpr int kChunk = 16;           // most query heads of a block's item
+
 struct AttendArgs {
   Cache cache;
   Pages pages;
   const uint16_t *q;
   int64_t q_stride;
-  int q_heads;
+  int q_heads, group;                // query heads, and how many share a cache head
+  int chunks, chunk;                 // chunks of a group, heads of a chunk
+  uint32_t div_mul;                  // t / page_size = (t * div_mul) >> div_shift, t < 2^31
+  int div_shift;
   const int32_t *lens;
-  float scale;
+  float scale_log2;                  // scale * log2(e): the softmax runs in powers of two
   int window;
   uint16_t *out;
   float *lse;
+  float *part;                       // [blocks][2][chunk][D + 4]: output, maximum, sum
+  int4 *joins;                       // [blocks]: item and last block of a shared item, by its first block
 };
 
-// One block of 4 warps per sequence and query head: every warp takes each
-// fourth token with its own running maximum and sum; joined at the end.
+// Tokens [first, end) of sequence b.
+__device__ __forceinline__ void token_range(const AttendArgs &a, int b, int &first, int &end, bool &over) {
+  const int room = a.pages.max_pages * a.cache.page_size;  // at most 2^30
+  const int len = a.lens[b];
+  over = len > room;
+  end = over ? room : max(len, 0);
+  first = a.window && end > a.window ? end - a.window : 0;
+}
+
+__device__ __forceinline__ int tiles_of(const AttendArgs &a, int b) {
+  int first, end;
+  bool over;
+  token_range(a, b, first, end, over);
+  return (end - first + kTile - 1) / kTile;
+}
+
+// Position of 16-byte piece `piece` of row `row` in a stage: the pieces of a
+// row are exchanged so that the 8 lanes of a shared-memory phase hit different
+// banks in all three accesses: the copies (one row), the keys (rows 2 i and
+// 2 i + 1, pieces 0..3 or 4..7) and the values (every other of 8 rows, pieces 2 i
+// and 2 i + 1).
+__device__ __forceinline__ int swizzle(int row, int piece) { return piece ^ ((row & 6) ^ ((row & 1) << 2)); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+  const int bytes = live ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four output elements from d on of query head h, and at d = 0 its lse.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv_attend_kernel(AttendArgs a, unsigned int *__restrict__ status) {
-  constexpr int V = D / 32;
-  __shared__ float part[4][D + 2];
+__device__ __forceinline__ void write_out(const AttendArgs &a, int b, int h, int d, float4 o, float base, float sum) {
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const int64_t at = static_cast<int64_t>(b) * a.q_heads + h;
+  *reinterpret_cast<uint2 *>(a.out + at * D + d) = make_uint2(T::pack(o.x * inv, o.y * inv), T::pack(o.z * inv, o.w * inv));
+  if (d == 0 && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994531f;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs a, unsigned int *__restrict__ status) {
+  constexpr int kStages = D == 64 ? 4 : 3;
+  constexpr int kRow = 2 * D;                 // bytes of a row
+  constexpr int kStage = 2 * 16 * kRow;       // 16 keys, 16 values
+  constexpr int kPieces = D / 8;
+  constexpr int kRowsPer = 32 / kPieces;      // rows that one copy instruction of a warp covers
+  constexpr int kPart = D + 4;                // floats of a partial result
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint32_t live_rows[kAttendWarps][kStages];
+  __shared__ int64_t sums[kAttendWarps + 1];
+  __shared__ int64_t found[2];                // start of the sequence that the share begins in, its number
   griddep_launch_dependents();
   griddep_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.x / a.q_heads, h = blockIdx.x % a.q_heads;
-  const int kvh = h / (a.q_heads / a.cache.heads);
-  const int64_t room = static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size;
-  int64_t len = a.lens[b];
-  if (len > room) {
-    len = room;
-    if (threadIdx.x == 0) atomicOr(status, W4A4_DEV_RANGE);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const int B = a.pages.n_seqs;
+  const int per_seq = a.cache.heads * a.chunks;  // items of a sequence
+
+  // The line of tiles: every thread adds up its run of sequences.
+  const int run = (B + 127) / 128;
+  int64_t mine = 0;
+  for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
+    int first, end;
+    bool over;
+    token_range(a, b, first, end, over);
+    if (over && blockIdx.x == 0) atomicOr(status, W4A4_DEV_RANGE);
+    mine += static_cast<int64_t>((end - first + kTile - 1) / kTile) * per_seq;
   }
-  const int64_t first = a.window && len > a.window ? len - a.window : 0;
-  float q[V], acc[V], m = -INFINITY, l = 0.0f;
-  for (int i = 0; i < V; ++i) {
-    q[i] = T::to_f32(a.q[b * a.q_stride + h * D + lane + 32 * i]);
-    acc[i] = 0.0f;
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
   }
-  for (int64_t t = first + warp; t < len; t += 4) {
-    const int page = a.pages.table[b * static_cast<int64_t>(a.pages.max_pages) + t / a.cache.page_size];
-    if (page < 0 || page >= a.cache.n_pages) {
-      if (lane == 0) atomicOr(status, W4A4_DEV_RANGE);
-      continue;
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kAttendWarps; ++w) {
+    if (w < warp) upto += sums[w];
+    total += sums[w];
+  }
+  // Nothing to attend to: zeros, spread over the blocks.
+  for (int b = blockIdx.x; b < B; b += gridDim.x)
+    if (tiles_of(a, b) == 0) {
+      for (int i = tid; i < a.q_heads * D / 8; i += 128)
+        reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(b) * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.lse)
+        for (int i = tid; i < a.q_heads; i += 128) a.lse[static_cast<int64_t>(b) * a.q_heads + i] = -INFINITY;
     }
-    const int64_t at = page * a.cache.stride_page + (t % a.cache.page_size) * a.cache.stride_token +
-                       kvh * a.cache.stride_head + lane;
-    float s = 0.0f;
-    for (int i = 0; i < V; ++i) s = fmaf(q[i], T::to_f32(a.cache.k[at + 32 * i]), s);
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    s *= a.scale;
-    const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn;
-    const float keep = expf(m - base), p = expf(s - base);
-    l = l * keep + p;
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * keep + p * T::to_f32(a.cache.v[at + 32 * i]);
-    m = mn;
+  const int64_t blocks = total < gridDim.x ? total : gridDim.x;  // no share is empty
+  if (blockIdx.x >= blocks) {
+    if (tid == 0) a.joins[blockIdx.x].x = -1;
+    return;
   }
-  for (int i = 0; i < V; ++i) part[warp][lane + 32 * i] = acc[i];
-  if (lane == 0) {
-    part[warp][D] = m;
-    part[warp][D + 1] = l;
+  const int64_t begin = blockIdx.x * total / blocks, stop = (blockIdx.x + 1) * total / blocks;
+  if (upto - mine <= begin && begin < upto) {
+    int64_t at = upto - mine;
+    int b = tid * run;
+    for (;; ++b) {
+      const int64_t n = static_cast<int64_t>(tiles_of(a, b)) * per_seq;
+      if (begin < at + n) break;
+      at += n;
+    }
+    found[0] = at;
+    found[1] = b;
   }
   __syncthreads();
-  float top = -INFINITY, total = 0.0f;
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][D]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float f[4];
-  for (int w = 0; w < 4; ++w) {
-    f[w] = expf(part[w][D] - base);
-    total += f[w] * part[w][D + 1];
+  int64_t seq_at = found[0];
+  int b = static_cast<int>(found[1]);
+  bool absent = false;
+  int4 join = make_int4(-1, 0, 0, 0);
+
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  for (int64_t u = begin; u < stop;) {
+    int first, end;
+    bool over;
+    token_range(a, b, first, end, over);
+    const int tiles = (end - first + kTile - 1) / kTile;
+    if (u >= seq_at + static_cast<int64_t>(tiles) * per_seq) {  // the next sequence
+      seq_at += static_cast<int64_t>(tiles) * per_seq;
+      ++b;
+      continue;
+    }
+    const int item = static_cast<int>((u - seq_at) / tiles);
+    const int t0 = static_cast<int>((u - seq_at) % tiles);
+    const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (stop - u)));
+    const int kvh = item / a.chunks;
+    const int h0 = (item % a.chunks) * a.chunk;            // first head of the chunk, in its group
+    const int heads = min(a.chunk, a.group - h0);
+    const uint16_t *qrow = a.q + b * a.q_stride + static_cast<int64_t>(kvh * a.group + h0) * D;
+    const int from = first + t0 * kTile, to = min(end, first + t1 * kTile);
+    const int subs = (to - from + 15) / 16;                // 16-token pieces; this warp: warp, warp + 4, ...
+
+    // The row of token from + 16 i + lane % 16 in the cache, or -1.
+    const int32_t *table = a.pages.table + static_cast<int64_t>(b) * a.pages.max_pages;
+    auto row_of = [&](int i) -> int64_t {
+      const int t = from + 16 * i + (lane & 15);
+      if (t >= to || t < from) return -1;
+      const int entry = static_cast<int>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
+      const int page = __ldg(table + entry);
+      if (page < 0 || page >= a.cache.n_pages) {
+        absent = true;
+        return -1;
+      }
+      return page * a.cache.stride_page + (t - entry * a.cache.page_size) * a.cache.stride_token;
+    };
+    const uint16_t *kbase = a.cache.k + kvh * a.cache.stride_head;
+    const uint16_t *vbase = a.cache.v + kvh * a.cache.stride_head;
+    auto fill = [&](int stage, int64_t row) {
+      const uint32_t dst = ring + stage * kStage;
+      const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+      if (lane == 0) live_rows[warp][stage] = live & 0xFFFFu;
+#pragma unroll
+      for (int i = 0; i < 16 / kRowsPer; ++i) {
+        const int rr = i * kRowsPer + lane / kPieces, piece = lane % kPieces;
+        const int64_t off = __shfl_sync(0xffffffffu, row, rr);
+        const bool ok = off >= 0;
+        const int64_t at = off + piece * 8;
+        const uint32_t to_ = dst + rr * kRow + swizzle(rr, piece) * 16;
+        copy16(to_, ok ? kbase + at : a.q, ok);
+        copy16(to_ + 16 * kRow, ok ? vbase + at : a.q, ok);
+      }
+    };
+    int ahead = warp;                                       // next piece to fill
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+      if (ahead < subs) fill(s, row_of(ahead));
+      copy_commit();
+      ahead += kAttendWarps;
+    }
+    int64_t next_row = ahead < subs ? row_of(ahead) : -1;
+
+    // queries: pieces c, c + 4, ... of rows r and r + 8, as the keys' lanes read theirs
+    uint4 q0[D / 32], q1[D / 32];
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      q0[j] = r < heads ? *reinterpret_cast<const uint4 *>(qrow + r * D + 8 * (c + 4 * j)) : make_uint4(0u, 0u, 0u, 0u);
+      q1[j] = NT == 2 && r + 8 < heads ? *reinterpret_cast<const uint4 *>(qrow + (r + 8) * D + 8 * (c + 4 * j))
+                                       : make_uint4(0u, 0u, 0u, 0u);
+    }
+    float acc[NT][D / 16][4];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n] = -INFINITY;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
+    }
+
+    int stage = 0;
+    for (int sub = warp; sub < subs; sub += kAttendWarps) {
+      copy_wait<kStages - 2>();
+      __syncwarp();
+      // the stage that was read last round takes the piece kStages - 1 ahead
+      {
+        const int s = stage == 0 ? kStages - 1 : stage - 1;
+        if (ahead < subs) fill(s, next_row);
+        copy_commit();
+        ahead += kAttendWarps;
+        next_row = ahead < subs ? row_of(ahead) : -1;
+      }
+      const uint32_t keys = ring + stage * kStage, values = keys + 16 * kRow;
+      float s[2][4];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = 0.0f;
+        const int row = 8 * t + r;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 k = lds16(keys + row * kRow + swizzle(row, c + 4 * j) * 16);
+          T::mma(s[t], q0[j].x, q1[j].x, q0[j].y, q1[j].y, k.x, k.y);
+          T::mma(s[t], q0[j].z, q1[j].z, q0[j].w, q1[j].w, k.z, k.w);
+        }
+      }
+      const uint32_t live = live_rows[warp][stage];
+      uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x[4] = {s[0][2 * n] * a.scale_log2, s[0][2 * n + 1] * a.scale_log2, s[1][2 * n] * a.scale_log2,
+                      s[1][2 * n + 1] * a.scale_log2};
+        if (live != 0xFFFFu) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!((live >> (8 * (e >> 1) + 2 * c + (e & 1))) & 1u)) x[e] = -INFINITY;
+        }
+        float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m[n], top);
+        const float base = mn == -INFINITY ? 0.0f : mn;
+        if (__any_sync(0xffffffffu, mn != m[n])) {
+          const float keep = exp2f(m[n] - base);
+          l[n] *= keep;
+          // outputs lie by head 2 c, 2 c + 1: their factors are in the lanes of those heads
+          const float k0 = __shfl_sync(0xffffffffu, keep, 8 * c), k1 = __shfl_sync(0xffffffffu, keep, 8 * c + 4);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            acc[n][i][0] *= k0;
+            acc[n][i][1] *= k1;
+            acc[n][i][2] *= k0;
+            acc[n][i][3] *= k1;
+          }
+          m[n] = mn;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = ex2(x[e] - base);
+        l[n] += (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          hi[n][t] = T::pack(x[2 * t], x[2 * t + 1]);
+          lo[n][t] = T::pack(x[2 * t] - T::lo(hi[n][t]), x[2 * t + 1] - T::hi(hi[n][t]));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = 2 * c + (i & 1) + 8 * (i >> 1);
+          v[i] = lds16(values + row * kRow + swizzle(row, r + 8 * j) * 16);
+        }
+        const uint32_t w[4][4] = {{v[0].x, v[0].y, v[0].z, v[0].w}, {v[1].x, v[1].y, v[1].z, v[1].w},
+                                  {v[2].x, v[2].y, v[2].z, v[2].w}, {v[3].x, v[3].y, v[3].z, v[3].w}};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // rows of A: dims 64 j + 8 r + 2 i (lanes' first) and + 1; columns: tokens
+          const uint32_t a0 = __byte_perm(w[0][i], w[1][i], 0x5410), a1 = __byte_perm(w[0][i], w[1][i], 0x7632);
+          const uint32_t a2 = __byte_perm(w[2][i], w[3][i], 0x5410), a3 = __byte_perm(w[2][i], w[3][i], 0x7632);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            T::mma(acc[n][4 * j + i], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+            T::mma(acc[n][4 * j + i], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+          }
+        }
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    __syncthreads();                                        // the rings are free: they take the warps' results
+    float *box = reinterpret_cast<float *>(smem);           // [warp][head][kPart]
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 1);
+      l[n] += __shfl_xor_sync(0xffffffffu, l[n], 2);
+      if (c == 0) {
+        box[(warp * 8 * NT + 8 * n + r) * kPart + D] = m[n];
+        box[(warp * 8 * NT + 8 * n + r) * kPart + D + 1] = l[n];
+      }
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float2 *>(
+              &box[(warp * 8 * NT + 8 * n + 2 * c + e) * kPart + 64 * (i / 4) + 8 * r + 2 * (i % 4)]) =
+              make_float2(acc[n][i][e], acc[n][i][2 + e]);
+    }
+    __syncthreads();
+    const bool whole = t0 == 0 && t1 == tiles;
+    const int slot = u == begin ? 0 : 1;
+    for (int i = tid; i < heads * (D / 4); i += 128) {
+      const int h = i / (D / 4), d = 4 * (i % (D / 4));
+      float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w) top = fmaxf(top, box[(w * 8 * NT + h) * kPart + D]);
+      const float base = top == -INFINITY ? 0.0f : top;
+      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kAttendWarps; ++w) {
+        const float *p = &box[(w * 8 * NT + h) * kPart];
+        const float f = exp2f(p[D] - base);
+        sum = fmaf(f, p[D + 1], sum);
+        const float4 v = *reinterpret_cast<const float4 *>(p + d);
+        o.x = fmaf(f, v.x, o.x);
+        o.y = fmaf(f, v.y, o.y);
+        o.z = fmaf(f, v.z, o.z);
+        o.w = fmaf(f, v.w, o.w);
+      }
+      if (whole) {
+        write_out<T, D>(a, b, kvh * a.group + h0 + h, d, o, base, sum);
+      } else {
+        float *p = a.part + ((static_cast<int64_t>(blockIdx.x) * 2 + slot) * a.chunk + h) * kPart;
+        *reinterpret_cast<float4 *>(p + d) = o;
+        if (d == 0) *reinterpret_cast<float2 *>(p + D) = make_float2(top, sum);
+      }
+    }
+    if (!whole && t0 == 0) {
+      // the block that holds the item's last tile: block i's share ends at (i + 1) total / blocks
+      const int64_t last = u + tiles - 1;
+      join = make_int4(b, item, slot, static_cast<int>(((last + 1) * blocks - 1) / total));
+    }
+    __syncthreads();                                        // before the rings are filled again
+    u += t1 - t0;
   }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float o = 0.0f;
-    for (int w = 0; w < 4; ++w) o += f[w] * part[w][d];
-    a.out[(static_cast<int64_t>(b) * a.q_heads + h) * D + d] = T::round(total == 0.0f ? 0.0f : o / total);
+  if (absent) atomicOr(status, W4A4_DEV_RANGE);
+  if (tid == 0) a.joins[blockIdx.x] = join;
+}
+
+// One block per shared item and head: parts of blocks i..last, by 16-byte pieces.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv_join_kernel(AttendArgs a, int blocks) {
+  constexpr int kPart = D + 4, kLanes = D / 4, kGroups = 256 / kLanes;
+  __shared__ float weight[kMaxBlocks];
+  __shared__ float red[16];
+  __shared__ int jobs[kMaxBlocks];
+  __shared__ int n_jobs;
+  __shared__ float4 box[kGroups][kLanes];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (warp == 0) {  // the blocks that begin a shared item, in order
+    int n = 0;
+    for (int i = 0; i < blocks; i += 32) {
+      const bool lead = i + lane < blocks && a.joins[i + lane].x >= 0;
+      const uint32_t all = __ballot_sync(0xffffffffu, lead);
+      if (lead) jobs[n + __popc(all & ((1u << lane) - 1u))] = i + lane;
+      n += __popc(all);
+    }
+    if (lane == 0) n_jobs = n;
   }
-  if (a.lse && threadIdx.x == 0)
-    a.lse[static_cast<int64_t>(b) * a.q_heads + h] = total == 0.0f ? -INFINITY : base + logf(total);
+  __syncthreads();
+  for (int job = blockIdx.x; job < n_jobs * a.chunk; job += gridDim.x) {
+    const int lead = jobs[job / a.chunk], h = job % a.chunk;
+    const int4 j = a.joins[lead];
+    const int kvh = j.y / a.chunks, h0 = (j.y % a.chunks) * a.chunk;
+    if (h >= min(a.chunk, a.group - h0)) continue;
+    const int parts = j.w - lead + 1;
+    auto part = [&](int i) {
+      return a.part + ((static_cast<int64_t>(lead + i) * 2 + (i == 0 ? j.z : 0)) * a.chunk + h) * kPart;
+    };
+    float top = -INFINITY;
+    for (int i = tid; i < parts; i += 256) {
+      weight[i] = part(i)[D];
+      top = fmaxf(top, weight[i]);
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[warp] = top;
+    __syncthreads();
+    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int i = tid; i < parts; i += 256) {
+      const float f = exp2f(weight[i] - base);
+      sum = fmaf(f, part(i)[D + 1], sum);
+      weight[i] = f;
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[8 + warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int w = 0; w < 8; ++w) sum += red[8 + w];
+    const int g = tid / kLanes, d = 4 * (tid % kLanes);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = g; i < parts; i += kGroups) {
+      const float f = weight[i];
+      const float4 v = *reinterpret_cast<const float4 *>(part(i) + d);
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    }
+    box[g][tid % kLanes] = o;
+    __syncthreads();
+    if (g == 0) {
+      for (int i = 1; i < kGroups; ++i) {
+        const float4 v = box[i][tid];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+      }
+      write_out<T, D>(a, j.x, kvh * a.group + h0 + h, d, o, base, sum);
+    }
+    __syncthreads();
+  }
 }
 
 w4a4_status check_cache(const w4a4_kv_cache_t *c, Cache *out) {
@@ -179,20 +593,54 @@ w4a4_status check_pages(const int32_t *pages, int32_t n_seqs, int32_t max_pages)
   return ptr_aligned4(pages) ? W4A4_OK : W4A4_ERR_ALIGN;
 }
 
-template <typename A>
-w4a4_status launch(void (*kern)(A, unsigned int *), int64_t grid, int threads, const A &args, void *stream) {
-  unsigned int *status = nullptr;
-  if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
+cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, args, status));
+  return cfg;
+}
+
+size_t part_bytes(int group, int D) {
+  const int chunks = (group + kChunk - 1) / kChunk, chunk = (group + chunks - 1) / chunks;
+  return static_cast<size_t>(kMaxBlocks) * 2 * chunk * (D + 4) * sizeof(float);
+}
+
+template <typename T, int D, int NT>
+w4a4_status launch_attend(AttendArgs &a, void *stream) {
+  constexpr int kStages = D == 64 ? 4 : 3;
+  constexpr int kRing = kAttendWarps * kStages * 2 * 16 * 2 * D, kBox = kAttendWarps * 8 * NT * (D + 4) * 4;
+  constexpr int kSmem = kRing > kBox ? kRing : kBox;
+  static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
+  int per_sm = 0;
+  if (occupancy.get(&per_sm, [](int *v) {
+        cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kSmem);
+        if (e == cudaSuccess)
+          e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kv_attend_kernel<T, D, NT>, 32 * kAttendWarps, kSmem);
+        return e;
+      }) != cudaSuccess || per_sm < 1)
+    return W4A4_ERR_CUDA;
+  unsigned int *status = nullptr;
+  if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
+  // blocks: one per place on the GPU, fewer when there cannot be that many tiles
+  int64_t grid = static_cast<int64_t>(device_sm_count()) * per_sm;
+  if (grid > kMaxBlocks) grid = kMaxBlocks;
+  const int64_t tiles = (static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size + kTile - 1) / kTile;
+  const int64_t items = static_cast<int64_t>(a.pages.n_seqs) * a.cache.heads * a.chunks;
+  if (tiles < grid && items < grid && items * tiles < grid) grid = items * tiles > 0 ? items * tiles : 1;
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
+  if (e != cudaSuccess || grid == 1) return launch_status(e);
+  const int64_t jobs = grid * a.chunk, most = 2ll * device_sm_count();
+  cfg = launch_config(jobs < most ? jobs : most, 256, 0, stream, &attr);
+  return launch_status(cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a, static_cast<int>(grid)));
 }
 
 }  // namespace
@@ -260,13 +708,18 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int6
   a.table_pos = table_pos;
   a.table = table;
   a.pairs = (flags & W4A4_FLAG_ROPE_PAIRS) != 0;
-  return launch((cache->flags & W4A4_FLAG_FP16) ? kv_append_kernel<Fp16> : kv_append_kernel<Bf16>, T, 128, a, stream);
+  unsigned int *status = nullptr;
+  if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = launch_config(T, 128, 0, stream, &attr);
+  auto kern = (cache->flags & W4A4_FLAG_FP16) ? kv_append_kernel<Fp16> : kv_append_kernel<Bf16>;
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, a, status));
 }
 
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (n_seqs < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
     return 0;
-  return 256;
+  return w4a4::part_bytes(n_q_heads / n_kv_heads, head_dim) + sizeof(int4) * w4a4::kMaxBlocks;
 }
 
 w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_heads, const w4a4_kv_cache_t *cache,
@@ -280,6 +733,7 @@ w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_head
   const int D = cache->head_dim;
   if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % a.cache.heads || window < 0) return W4A4_ERR_SHAPE;
   if ((st = check_pages(pages, n_seqs, max_pages)) != W4A4_OK) return st;
+  if (static_cast<int64_t>(max_pages) * a.cache.page_size > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
   if (!std::isfinite(scale)) return W4A4_ERR_ARG;
   if (n_seqs == 0) return W4A4_OK;
   if (!q || !lens || !out || !workspace) return W4A4_ERR_ARG;
@@ -293,16 +747,26 @@ w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_head
   a.q_stride = q_stride;
   a.q_heads = n_q_heads;
   a.lens = lens;
-  a.scale = scale;
+  a.group = n_q_heads / a.cache.heads;
+  a.chunks = (a.group + kChunk - 1) / kChunk;
+  a.chunk = (a.group + a.chunks - 1) / a.chunks;
+  int shift = 0;  // page_size <= 2^shift
+  while ((int64_t(1) << shift) < a.cache.page_size) ++shift;
+  a.div_shift = 31 + shift;
+  a.div_mul = static_cast<uint32_t>((uint64_t(1) << a.div_shift) / a.cache.page_size + 1);
+  a.scale_log2 = scale * 1.4426950408889634f;
   a.window = window;
   a.out = out;
   a.lse = lse;
-  const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0;
-  const int64_t grid = static_cast<int64_t>(n_seqs) * n_q_heads;
-  if (grid > 0x7FFFFFFF) return W4A4_ERR_SHAPE;
-  auto kern = D == 64 ? (fp16 ? kv_attend_kernel<Fp16, 64> : kv_attend_kernel<Bf16, 64>)
-                      : (fp16 ? kv_attend_kernel<Fp16, 128> : kv_attend_kernel<Bf16, 128>);
-  return launch(kern, grid, 128, a, stream);
+  a.part = static_cast<float *>(workspace);
+  a.joins = reinterpret_cast<int4 *>(static_cast<uint8_t *>(workspace) + part_bytes(a.group, D));
+  const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0, wide = a.chunk > 8;
+  if (D == 64) {
+    if (fp16) return wide ? launch_attend<Fp16, 64, 2>(a, stream) : launch_attend<Fp16, 64, 1>(a, stream);
+    return wide ? launch_attend<Bf16, 64, 2>(a, stream) : launch_attend<Bf16, 64, 1>(a, stream);
+  }
+  if (fp16) return wide ? launch_attend<Fp16, 128, 2>(a, stream) : launch_attend<Fp16, 128, 1>(a, stream);
+  return wide ? launch_attend<Bf16, 128, 2>(a, stream) : launch_attend<Bf16, 128, 1>(a, stream);
 }
 
 }  // extern "C"
