@@ -23,6 +23,15 @@ struct Bf16 {
     return *reinterpret_cast<const uint32_t *>(&h);
   }
   static __device__ __forceinline__ uint16_t round(float a) { return __bfloat16_as_ushort(__float2bfloat16_rn(a)); }
+  // The 8 codes of a word (4-bit two's complement, element 2 p in nibble p, 2 p + 1 in nibble p + 4) as 4 pairs:
+  // 2^7 + u with u = c + 8 in the low mantissa bits, minus 136; exact.
+  static __device__ __forceinline__ void codes(uint32_t w, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      const uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) ^ 0x43084308u;
+      asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[p]) : "r"(v), "r"(0x43084308u));
+    }
+  }
   // d (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums
   static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {
@@ -43,6 +52,17 @@ struct Fp16 {
     return *reinterpret_cast<const uint32_t *>(&h);
   }
   static __device__ __forceinline__ uint16_t round(float a) { return __half_as_ushort(__float2half_rn(a)); }
+  // As above with 2^10 + u; the nibbles at bits 4..7 stand for 16 u.
+  static __device__ __forceinline__ void codes(uint32_t w, uint32_t (&o)[4]) {
+#pragma unroll
+    for (int p = 0; p < 4; p += 2) {
+      const uint32_t v = w >> (4 * p);
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[p]) : "r"((v & 0x000F000Fu) ^ 0x64086408u), "r"(0x64086408u));
+      // (2^10 + 16 u) / 16 - 72
+      asm("fma.rn.f16x2 %0, %1, %2, %3;"
+          : "=r"(o[p + 1]) : "r"((v & 0x00F000F0u) ^ 0x64806480u), "r"(0x2C002C00u), "r"(0xD480D480u));
+    }
+  }
   // d (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums
   static __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                              uint32_t b0, uint32_t b1) {

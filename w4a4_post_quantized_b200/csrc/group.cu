@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include "ctxcache.h"
 #include "decode.cuh"
 #include "decode.h"
 #include "gelu.cuh"
@@ -124,38 +125,201 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// One warp per row and token: lane l takes words l, l + 32, ... of the row.
-template <typename T>
-__global__ void __launch_bounds__(256)
-    group_gemv_kernel(const uint16_t *__restrict__ X, int M, const uint8_t *__restrict__ codes,
-                      const uint16_t *__restrict__ scales, GroupShape s, const uint16_t *__restrict__ bias,
-                      uint16_t *__restrict__ Y, bool gelu) {
+// -------------------------------------------------------------------- gemv
+//
+// Y[m, n] = sum_g s[n, g] sum_{k in g} c[n, k] x[m, k] + b[n] for at most 16
+// tokens m.  Every code is read once and used M times: bound by the weights'
+// traffic, N K / 2 bytes and the steps.  What the SMs have to do meanwhile is turn
+// 8 codes per 4 bytes into operands, so products run as m16n8k16 on the tensor
+// cores (A = 16 rows of weights, B = 8 tokens; a 128-row tcgen05 tile with one to
+// 16 columns would read its operands from shared memory, to which every widened
+// weight would have to be written first).
+//
+//  * The packed order is that of the operand: the 16 bytes that a lane copies
+//    are its codes of one row of A for 8 products, no exchange between lanes.
+//    In a word, elements 2 p and 2 p + 1 are nibbles p and p + 4, so one masked
+//    xor gives a pair of 16-bit values 2^7 + u (bf16) or 2^10 + u, u = c + 8, and a
+//    subtraction the exact codes.
+//  * A group's products are summed in fp32 by the tensor core, multiplied by the
+//    step and added to the fp32 total: the codes stay exact and no weight is rounded.
+//  * A block of 8 warps takes rows in tiles, its warps an eighth of the inputs each;
+//    a warp streams its codes and steps through its own ring of asynchronous copies,
+//    across the ends of tiles, and the eight sums meet in shared memory.
+//  * Before it waits for the kernel in front, a block asks for its first weights
+//    to be brought into L2: those do not depend on that kernel, and where they do
+//    (a quantization right before) L2 is where the new values appear.
+
+constexpr int kGemvWarps = 8;
+
+struct GemvArgs {
+  const uint16_t *X;
+  int M;
+  const uint8_t *codes;
+  const uint16_t *scales;
+  GroupShape s;
+  const uint16_t *bias;
+  uint16_t *Y;
+  bool gelu;
+};
+
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// GROUP inputs per step, RT tiles of 16 rows per block, NT times 8 tokens.
+template <typename T, int GROUP, int RT, int NT>
+__global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs a) {
+  constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
+  constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
+  constexpr int kStage = RT * (1024 + 8 * kScaleRow);
+  constexpr int kStages = RT == 1 ? 8 : 5;
+  constexpr int kRows = 16 * RT, kCols = 8 * NT;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float sums[2][kGemvWarps][kCols][kRows + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int r = lane >> 2, c = lane & 3;
+  const GroupShape &s = a.s;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(warp) * s.blocks / kGemvWarps);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks / kGemvWarps);
+  const int row_groups = (s.tiles + RT - 1) / RT;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+
+  auto tile_at = [&](int rg, int t, int kb) {
+    return static_cast<int64_t>(min(rg * RT + t, s.tiles - 1)) * s.blocks + kb;
+  };
   griddep_launch_dependents();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = blockIdx.x * 8ll + (threadIdx.x >> 5);
-  const int n = static_cast<int>(unit / M), m = static_cast<int>(unit % M);
-  if (n >= s.N) return;
-  float sum = 0.0f;
-  for (int i = lane; i < s.K / 8; i += 32) {
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + word_offset(s, n, i));
-    const uint4 v = *reinterpret_cast<const uint4 *>(X + static_cast<int64_t>(m) * s.K + 8 * i);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    float part = 0.0f;
+  for (int kb = kb0; kb < min(kb1, kb0 + kStages); ++kb)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      part = fmaf(T::lo(u[e]), static_cast<float>(code_of(w, 2 * e)), part);
-      part = fmaf(T::hi(u[e]), static_cast<float>(code_of(w, 2 * e + 1)), part);
+    for (int t = 0; t < RT; ++t)
+      if (lane < 8) prefetch_l2(a.codes + tile_at(blockIdx.x, t, kb) * 1024 + 128 * lane);
+  griddep_wait();
+
+  // the copy stream: (row group, block of inputs) pairs in order
+  int copy_rg = blockIdx.x, copy_kb = kb0, copy_stage = 0;
+  auto fill = [&]() {
+    if (kb0 < kb1 && copy_rg < row_groups) {
+      const uint32_t dst = ring + copy_stage * kStage;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const int64_t at = tile_at(copy_rg, t, copy_kb);
+        copy16(dst + t * 1024 + 16 * lane, a.codes + at * 1024 + 16 * lane);
+        copy16(dst + t * 1024 + 512 + 16 * lane, a.codes + at * 1024 + 512 + 16 * lane);
+        if (lane < 8)
+          copy_small<kScaleRow>(dst + RT * 1024 + (t * 8 + lane) * kScaleRow,
+                                a.scales + (at * 8 + lane) * (kScaleRow / 2));
+      }
+      copy_stage = copy_stage == kStages - 1 ? 0 : copy_stage + 1;
+      if (++copy_kb == kb1) {
+        copy_kb = kb0;
+        copy_rg += gridDim.x;
+      }
     }
-    sum = fmaf(T::to_f32(scales[scale_offset(s, n, 8 * i / s.group)]), part, sum);
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fill();
+
+  int stage = 0, parity = 0;
+  for (int rg = blockIdx.x; rg < row_groups; rg += gridDim.x, parity ^= 1) {
+    float total[RT][NT][4];
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      // tokens r, r + 8 as the B operand: inputs 32 j + 8 c .. + 7 of the block
+      uint4 x[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = kb * kBlockK + 32 * j + 8 * c;
+          x[n][j] = make_uint4(0u, 0u, 0u, 0u);
+          if (8 * n + r < a.M && k < s.K)
+            x[n][j] = __ldg(reinterpret_cast<const uint4 *>(a.X + static_cast<int64_t>(8 * n + r) * s.K + k));
+        }
+      copy_wait<kStages - 2>();
+      __syncwarp();
+      fill();
+      const uint32_t base = ring + stage * kStage;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        uint4 w0, w1;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w0.x), "=r"(w0.y), "=r"(w0.z), "=r"(w0.w) : "r"(base + t * 1024 + 16 * lane));
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w1.x), "=r"(w1.y), "=r"(w1.z), "=r"(w1.w) : "r"(base + t * 1024 + 512 + 16 * lane));
+        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
+        float part[NT][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j % (GROUP / 32) == 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) part[n][e] = 0.0f;
+          }
+          uint32_t p[4], q[4];
+          T::codes(lo[j], p);
+          T::codes(hi[j], q);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            T::mma(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
+            T::mma(part[n], p[2], q[2], p[3], q[3], x[n][j].z, x[n][j].w);
+          }
+          if ((j + 1) % (GROUP / 32) == 0) {
+            uint32_t steps;
+            asm volatile("ld.shared.u32 %0, [%1];"
+                         : "=r"(steps)
+                         : "r"(base + RT * 1024 + (t * 8 + r) * kScaleRow + 4 * (j / (GROUP / 32))));
+            const float s0 = T::lo(steps), s1 = T::hi(steps);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              total[t][n][0] = fmaf(s0, part[n][0], total[t][n][0]);
+              total[t][n][1] = fmaf(s0, part[n][1], total[t][n][1]);
+              total[t][n][2] = fmaf(s1, part[n][2], total[t][n][2]);
+              total[t][n][3] = fmaf(s1, part[n][3], total[t][n][3]);
+            }
+          }
+        }
+      }
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+    }
+    // the eighths meet; two sets of sums, so one barrier per row group is enough
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          sums[parity][warp][8 * n + 2 * c + (e & 1)][16 * t + r + 8 * (e >> 1)] = total[t][n][e];
+    __syncthreads();
+    for (int i = tid; i < kRows * a.M; i += 32 * kGemvWarps) {
+      const int row = i % kRows, m = i / kRows;
+      const int64_t n = static_cast<int64_t>(rg) * kRows + row;
+      if (n >= s.N) continue;
+      float y = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kGemvWarps; ++w) y += sums[parity][w][m][row];
+      if (a.bias) y += T::to_f32(a.bias[n]);
+      uint16_t v = T::round(y);
+      if (a.gelu) v = static_cast<uint16_t>(gelu_pair_bf16(v) & 0xFFFFu);
+      a.Y[m * static_cast<int64_t>(s.N) + n] = v;
+    }
   }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) {
-    if (bias) sum += T::to_f32(bias[n]);
-    uint16_t y = T::round(sum);
-    if (gelu) y = static_cast<uint16_t>(gelu_pair_bf16(y) & 0xFFFFu);
-    Y[static_cast<int64_t>(m) * s.N + n] = y;
-  }
+  copy_wait<0>();
 }
 
 constexpr uint32_t kGroupFlags = W4A4_FLAG_FP16;
@@ -203,6 +367,33 @@ cudaError_t launch(void (*kern)(P...), int64_t grid, int threads, size_t smem, v
 int64_t stride_grid(int64_t n) {
   const int64_t need = (n + 255) / 256, most = 16ll * device_sm_count();
   return need < most ? need : most;
+}
+
+template <typename T, int GROUP, int RT, int NT>
+w4a4_status launch_gemv_t(const GemvArgs &a, void *stream) {
+  constexpr int kSmem = kGemvWarps * (RT == 1 ? 8 : 5) * RT * (1024 + 8 * 4 * (kBlockK / GROUP));
+  static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
+  int per_sm = 0;
+  if (occupancy.get(&per_sm, [](int *v) {
+        cudaError_t e = cudaFuncSetAttribute(group_gemv_kernel<T, GROUP, RT, NT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess)
+          e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, group_gemv_kernel<T, GROUP, RT, NT>, 32 * kGemvWarps,
+                                                            kSmem);
+        return e;
+      }) != cudaSuccess || per_sm < 1)
+    return W4A4_ERR_CUDA;
+  const int64_t need = (a.s.tiles + RT - 1) / RT, most = static_cast<int64_t>(device_sm_count()) * per_sm;
+  return launch_status(
+      launch(group_gemv_kernel<T, GROUP, RT, NT>, need < most ? need : most, 32 * kGemvWarps, kSmem, stream, a));
+}
+
+template <typename T, int GROUP>
+w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
+  // two tiles per block share every token operand; one where that would leave SMs idle
+  const bool two = a.s.tiles >= 4 * device_sm_count();
+  if (a.M <= 8) return two ? launch_gemv_t<T, GROUP, 2, 1>(a, stream) : launch_gemv_t<T, GROUP, 1, 1>(a, stream);
+  return two ? launch_gemv_t<T, GROUP, 2, 2>(a, stream) : launch_gemv_t<T, GROUP, 1, 2>(a, stream);
 }
 
 }  // namespace
@@ -283,11 +474,12 @@ w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weigh
   if (M == 0) return W4A4_OK;
   if (!X || !Y) return W4A4_ERR_ARG;
   if (!ptr_aligned16(X) || !ptr_aligned16(Y) || (bias && !ptr_aligned16(bias))) return W4A4_ERR_ALIGN;
-  const GroupShape s = shape_of(w->N, w->K, w->group);
-  const int64_t grid = (static_cast<int64_t>(s.N) * M + 7) / 8;
-  if (grid > 0x7FFFFFFF) return W4A4_ERR_SHAPE;
-  return launch_status(launch(fp16 ? group_gemv_kernel<Fp16> : group_gemv_kernel<Bf16>, grid, 256, 0, stream, X,
-                              static_cast<int>(M), w->codes, w->scales, s, bias, Y, gelu));
+  const GemvArgs a{X, static_cast<int>(M), w->codes, w->scales, shape_of(w->N, w->K, w->group), bias, Y, gelu};
+  switch (w->group) {
+    case 32: return fp16 ? launch_gemv<Fp16, 32>(a, stream) : launch_gemv<Bf16, 32>(a, stream);
+    case 64: return fp16 ? launch_gemv<Fp16, 64>(a, stream) : launch_gemv<Bf16, 64>(a, stream);
+    default: return fp16 ? launch_gemv<Fp16, 128>(a, stream) : launch_gemv<Bf16, 128>(a, stream);
+  }
 }
 
 }  // extern "C"
