@@ -55,7 +55,7 @@ extern "C" {
  * words, word j the 8 codes of inputs 32 j + 8 c + 0..7 of the block, inputs
  * 0, 2, 4, 6, 1, 3, 5, 7 from the lowest nibble up. */
 typedef struct {
-    int32_t N;         /* rows, >= 1 */
+    int32_t N;         /* rows, 1 .. 16777216 */
     int32_t K;         /* inputs, a positive multiple of group, <= 1048576 */
     int32_t group;     /* 32, 64 or 128 */
     uint32_t flags;    /* 0 or W4A4_FLAG_FP16: type of steps, weights and tokens */

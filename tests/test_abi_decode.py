@@ -65,7 +65,8 @@ def test_group_weights_layout(lib):
         assert out.codes == A and out.scales == A + (codes + 255) // 256 * 256
         assert lib.w4a4_group_bind(A, bytes_(N, K, g) - 1, N, K, g, 0, ctypes.byref(out)) == SHAPE
     for N, K, g in [(0, 512, 64), (-1, 512, 64), (256, 0, 64), (256, 96, 64), (256, 512, 16), (256, 512, 256),
-                    (256, (1 << 20) + 128, 128), (0x7FFFFFFF, 128, 128)]:
+                    (256, (1 << 20) + 128, 128), (0x7FFFFFFF, 128, 128),
+                    ((1 << 24) + 1, 128, 128)]:
         assert bytes_(N, K, g) == 0
     out = GroupT()
     assert lib.w4a4_group_bind(None, 1 << 30, 16, 128, 128, 0, ctypes.byref(out)) == ARG

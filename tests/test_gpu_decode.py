@@ -89,6 +89,29 @@ def test_quantize_and_back(w4, N, K, group, dt):
     assert torch.equal(w4.w4a4_group_dequantize(w).cpu(), dense(codes, steps, group).to(dt))
 
 
+@pytest.mark.parametrize("dt,power", [(BF16, -120), (BF16, -128), (BF16, -131), (FP16, -22), (FP16, 10), (BF16, 100)])
+def test_quantize_at_the_ends_of_the_range(w4, dt, power):
+    """Steps below the normal range, whose own rounding sends codes to the clamp,
+    and whose reciprocal would overflow; and large ones."""
+    W = (torch.randn(48, 256, generator=gen(7)) * 2.0 ** power).to(dt)
+    codes, steps = oracle_quantize(W, 32)
+    w = w4.w4a4_group_quantize(W.cuda(), 32)
+    assert torch.equal(w4.w4a4_group_dequantize(w).cpu(), dense(codes, steps, 32).to(dt))
+
+
+def test_quantize_ties(w4):
+    """Every quotient that ends in one half, with steps of 1 and of odd numbers, goes to the even code."""
+    rows = []
+    for step in (1.0, 3.0, 5.0, 0.75, 127.0):
+        half = torch.arange(-13, 14, 2) * 0.5 * step
+        rows.append(torch.cat([half, torch.tensor([7 * step]), torch.zeros(32 - 15)]))
+    W = torch.stack(rows).to(FP16)                 # all exact in 11 bits
+    codes, steps = oracle_quantize(W, 32)
+    assert (codes[:, :14] % 2 == 0).all()
+    w = w4.w4a4_group_quantize(W.cuda(), 32)
+    assert torch.equal(w4.w4a4_group_dequantize(w).cpu(), dense(codes, steps, 32).to(FP16))
+
+
 @pytest.mark.parametrize("dt", [BF16, FP16])
 @pytest.mark.parametrize("N,K,group", SHAPES)
 def test_pack_gives_what_quantize_stores(w4, N, K, group, dt):

@@ -22,106 +22,184 @@ struct GroupShape {
   int tiles, blocks;  // ceil(N / 16), ceil(K / 128)
 };
 
-// Byte offset of the word that holds inputs 8 i .. 8 i + 7 of row n.
-__device__ __forceinline__ int64_t word_offset(const GroupShape &s, int n, int i) {
-  const int t = n / kTileRows, h = (n >> 3) & 1, r = n & 7;
-  const int b = i >> 4, j = (i >> 2) & 3, c = i & 3;
-  return ((static_cast<int64_t>(t) * s.blocks + b) * 2 + h) * 512 + 64 * r + 16 * c + 4 * j;
-}
-
-// Element offset of the step of row n, group g.
-__device__ __forceinline__ int64_t scale_offset(const GroupShape &s, int n, int g) {
-  const int t = n / kTileRows, h = (n >> 3) & 1, r = n & 7;
-  const int per = kBlockK / s.group, b = g / per;
-  return ((static_cast<int64_t>(t) * s.blocks + b) * 8 + r) * (2 * per) + 2 * (g % per) + h;
-}
-
 // Nibble of element e (0..7) in a word: 0, 2, 4, 6, 1, 3, 5, 7 from the lowest up.
 __device__ __forceinline__ int nibble_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
 
-__device__ __forceinline__ int code_of(uint32_t w, int e) {
-  return (static_cast<int>((w >> nibble_shift(e)) & 15u) ^ 8) - 8;
+// ------------------------------------------------- quantize, pack, dequantize
+//
+// One pass over the weights, bound by HBM (2 bytes in, half a byte and the steps
+// out, or back).  A warp takes one tile and block, 16 rows by 128 inputs, in the
+// packed order itself: lane 4 r + c holds, of rows r and r + 8, the inputs 32 j +
+// 8 c .. + 7 for j = 0..3, so that its codes are the 16 bytes it stores (a whole
+// warp's 512 in a row), a group's maximum needs two exchanges between four
+// lanes, and all eight 16-byte loads are in flight at once.  (One thread per 8
+// inputs, with the rows' order on both sides: 20000 x 8192 there and back took 411
+// us.)
+
+constexpr int kPackWarps = 8;
+
+struct Unit {
+  int64_t at;  // tile * blocks + block
+  int row, k;  // of this lane: rows row and row + 8, inputs k + 32 j
+};
+
+__device__ __forceinline__ bool unit_of_warp(const GroupShape &s, Unit &u) {
+  const int lane = threadIdx.x & 31;
+  u.at = static_cast<int64_t>(blockIdx.x) * kPackWarps + (threadIdx.x >> 5);
+  if (u.at >= static_cast<int64_t>(s.tiles) * s.blocks) return false;
+  const int t = static_cast<int>(u.at / s.blocks), b = static_cast<int>(u.at % s.blocks);
+  u.row = t * kTileRows + (lane >> 2);
+  u.k = b * kBlockK + 8 * (lane & 3);
+  return true;
 }
 
-// One thread per word; the 4, 8 or 16 threads of a group share its maximum.
-// Rows and inputs of the padding get zero codes and steps.
-template <typename T>
-__global__ void __launch_bounds__(256)
+// round-half-even(x / step) for |x| <= max, two's complement in the low 4 bits of
+// o.  x and step have at most 11 significant bits, so a quotient that is not half
+// an integer is at least 2^-13 away from one: x * inv (off by less than 2^-19)
+// rounded to multiples of 2^-16, which the sum with 1.5 * 2^7 does, is exact at the
+// halves and on the right side elsewhere; the sum with 1.5 * 2^23 then rounds to an
+// integer.
+__device__ __forceinline__ void quantize_pair(float x0, float x1, unsigned long long inv, uint32_t &o0, uint32_t &o1) {
+  const unsigned long long t = fma2(f2(x0, x1), inv, f2(192.0f, 192.0f));
+  float a, b;
+  f2_split(t, a, b);
+  o0 = __float_as_uint(a + 12582720.0f);
+  o1 = __float_as_uint(b + 12582720.0f);
+}
+
+__device__ __noinline__ int slow_code(float x, float step) {
+  return step > 0.0f ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, step)), -8.0f), 7.0f)) : 0;
+}
+
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(32 * kPackWarps)
     group_quantize_kernel(const uint16_t *__restrict__ W, GroupShape s, uint8_t *__restrict__ codes,
                           uint16_t *__restrict__ scales) {
+  constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;  // groups of a block, words j of a group
   griddep_launch_dependents();
   griddep_wait();
-  const int words = s.blocks * (kBlockK / 8);
-  const int64_t total = static_cast<int64_t>(s.tiles) * kTileRows * words;
-  const int lanes = s.group / 8;  // threads of a group
-  // every thread of a warp takes part in the shuffles: total is a multiple of 32
-  for (int64_t at = blockIdx.x * 256ll + threadIdx.x; at < total; at += gridDim.x * 256ll) {
-    const int n = static_cast<int>(at / words), i = static_cast<int>(at % words);
-    float x[8];
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (n < s.N && 8 * i < s.K) v = *reinterpret_cast<const uint4 *>(W + static_cast<int64_t>(n) * s.K + 8 * i);
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    float m = 0.0f;
+  Unit u;
+  if (!unit_of_warp(s, u)) return;
+  const int lane = threadIdx.x & 31;
+  uint4 v[2][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[2 * e] = T::lo(u[e]);
-      x[2 * e + 1] = T::hi(u[e]);
-      m = fmaxf(m, fmaxf(fabsf(x[2 * e]), fabsf(x[2 * e + 1])));
-    }
-    for (int o = 1; o < lanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint16_t step16 = T::round(__fdiv_rn(m, 7.0f));
-    const float step = T::to_f32(step16);
-    uint32_t w = 0;
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float q = step > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(x[e], step)), -8.0f), 7.0f) : 0.0f;
-      w |= (static_cast<uint32_t>(static_cast<int>(q)) & 15u) << nibble_shift(e);
+    for (int j = 0; j < 4; ++j) {
+      v[h][j] = make_uint4(0u, 0u, 0u, 0u);  // padding: zero codes and steps
+      if (u.row + 8 * h < s.N && u.k + 32 * j < s.K)
+        v[h][j] = __ldcs(
+            reinterpret_cast<const uint4 *>(W + static_cast<int64_t>(u.row + 8 * h) * s.K + u.k + 32 * j));
     }
-    *reinterpret_cast<uint32_t *>(codes + word_offset(s, n, i)) = w;
-    if (i % lanes == 0) scales[scale_offset(s, n, i / lanes)] = step16;
+  uint32_t steps[kPer];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t word[4];
+#pragma unroll
+    for (int g = 0; g < kPer; ++g) {
+      uint32_t top = 0;  // of the magnitudes, in pairs
+#pragma unroll
+      for (int j = g * kWords; j < (g + 1) * kWords; ++j) {
+        top = T::max2(top, T::max2(v[h][j].x & 0x7FFF7FFFu, v[h][j].y & 0x7FFF7FFFu));
+        top = T::max2(top, T::max2(v[h][j].z & 0x7FFF7FFFu, v[h][j].w & 0x7FFF7FFFu));
+      }
+      top = T::max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = T::max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const float m = fmaxf(T::lo(top), T::hi(top));
+      const uint16_t step16 = T::round(__fdiv_rn(m, 7.0f));
+      const float step = T::to_f32(step16);
+      steps[g] = h == 0 ? step16 : steps[g] | (static_cast<uint32_t>(step16) << 16);
+      const float inv = 1.0f / step;
+      // a step so small that its own rounding, or its reciprocal's range, matters
+      const bool plain = step >= 0x1p-100f && m * inv < 7.4f;
+#pragma unroll
+      for (int j = g * kWords; j < (g + 1) * kWords; ++j) {
+        const uint32_t x[4] = {v[h][j].x, v[h][j].y, v[h][j].z, v[h][j].w};
+        uint32_t w = 0;
+#pragma unroll
+        for (int p = 3; p >= 0; --p) {
+          uint32_t a, b;
+          if (plain) {
+            quantize_pair(T::lo(x[p]), T::hi(x[p]), f2(inv, inv), a, b);
+          } else {
+            a = static_cast<uint32_t>(slow_code(T::lo(x[p]), step));
+            b = static_cast<uint32_t>(slow_code(T::hi(x[p]), step));
+          }
+          w = (w << 4) | (__byte_perm(a, b, 0x5410) & 0x000F000Fu);
+        }
+        word[j] = w;
+      }
+    }
+    *reinterpret_cast<uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane) =
+        make_uint4(word[0], word[1], word[2], word[3]);
+  }
+  if ((lane & 3) == 0) {
+    uint32_t *to = reinterpret_cast<uint32_t *>(scales) + (u.at * 8 + (lane >> 2)) * kPer;
+#pragma unroll
+    for (int g = 0; g < kPer; ++g) to[g] = steps[g];
   }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * kPackWarps)
     group_pack_kernel(const uint8_t *__restrict__ plain, const uint16_t *__restrict__ steps, GroupShape s,
                       uint8_t *__restrict__ codes, uint16_t *__restrict__ scales) {
   griddep_launch_dependents();
   griddep_wait();
-  const int words = s.blocks * (kBlockK / 8);
-  const int64_t total = static_cast<int64_t>(s.tiles) * kTileRows * words;
-  const int lanes = s.group / 8;
-  for (int64_t at = blockIdx.x * 256ll + threadIdx.x; at < total; at += gridDim.x * 256ll) {
-    const int n = static_cast<int>(at / words), i = static_cast<int>(at % words);
-    const bool live = n < s.N && 8 * i < s.K;
-    uint32_t v = 0, w = 0;
-    if (live) v = *reinterpret_cast<const uint32_t *>(plain + static_cast<int64_t>(n) * (s.K / 2) + 4 * i);
+  Unit u;
+  if (!unit_of_warp(s, u)) return;
+  const int lane = threadIdx.x & 31, per = kBlockK / s.group;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << nibble_shift(e);
-    *reinterpret_cast<uint32_t *>(codes + word_offset(s, n, i)) = w;
-    if (i % lanes == 0) {
-      const int g = i / lanes;
-      scales[scale_offset(s, n, g)] = live ? steps[static_cast<int64_t>(n) * (s.K / s.group) + g] : uint16_t(0);
+  for (int h = 0; h < 2; ++h) {
+    const int n = u.row + 8 * h;
+    uint32_t word[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v = 0, w = 0;
+      if (n < s.N && u.k + 32 * j < s.K)
+        v = *reinterpret_cast<const uint32_t *>(plain + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << nibble_shift(e);
+      word[j] = w;
+    }
+    *reinterpret_cast<uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane) =
+        make_uint4(word[0], word[1], word[2], word[3]);
+    const int g0 = (u.k / kBlockK) * per, groups = s.K / s.group;
+    if ((lane & 3) < per) {
+      const int g = lane & 3;
+      scales[((u.at * 8 + (lane >> 2)) * per + g) * 2 + h] =
+          n < s.N && g0 + g < groups ? steps[static_cast<int64_t>(n) * groups + g0 + g] : uint16_t(0);
     }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256)
+template <typename T, int GROUP>
+__global__ void __launch_bounds__(32 * kPackWarps)
     group_dequantize_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, GroupShape s,
                             uint16_t *__restrict__ W) {
+  constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;
   griddep_launch_dependents();
   griddep_wait();
-  const int words = s.K / 8;
-  const int64_t total = static_cast<int64_t>(s.N) * words;
-  for (int64_t at = blockIdx.x * 256ll + threadIdx.x; at < total; at += gridDim.x * 256ll) {
-    const int n = static_cast<int>(at / words), i = static_cast<int>(at % words);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + word_offset(s, n, i));
-    const float step = T::to_f32(scales[scale_offset(s, n, 8 * i / s.group)]);
-    uint32_t o[4];
+  Unit u;
+  if (!unit_of_warp(s, u)) return;
+  const int lane = threadIdx.x & 31;
+  uint32_t steps[kPer];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      o[e] = T::pack(static_cast<float>(code_of(w, 2 * e)) * step, static_cast<float>(code_of(w, 2 * e + 1)) * step);
-    *reinterpret_cast<uint4 *>(W + static_cast<int64_t>(n) * s.K + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int g = 0; g < kPer; ++g)
+    steps[g] = reinterpret_cast<const uint32_t *>(scales)[(u.at * 8 + (lane >> 2)) * kPer + g];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane));
+    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t step = __byte_perm(steps[j / kWords], 0u, h ? 0x3232 : 0x1010);  // twice
+      uint32_t c[4];
+      T::codes(word[j], c);
+      // an exact code times a step, rounded once
+      if (u.row + 8 * h < s.N && u.k + 32 * j < s.K)
+        __stcs(reinterpret_cast<uint4 *>(W + static_cast<int64_t>(u.row + 8 * h) * s.K + u.k + 32 * j),
+               make_uint4(T::mul2(c[0], step), T::mul2(c[1], step), T::mul2(c[2], step), T::mul2(c[3], step)));
+    }
   }
 }
 
@@ -326,7 +404,7 @@ constexpr uint32_t kGroupFlags = W4A4_FLAG_FP16;
 
 bool group_ok(int32_t group) { return group == 32 || group == 64 || group == 128; }
 bool group_shape_ok(int32_t N, int32_t K, int32_t group) {
-  return N >= 1 && N <= 0x7FFFFFF0 && K >= group && K % group == 0 && K <= (1 << 20);
+  return N >= 1 && N <= (1 << 24) && K >= group && K % group == 0 && K <= (1 << 20);
 }
 
 GroupShape shape_of(int32_t N, int32_t K, int32_t group) {
@@ -363,10 +441,27 @@ cudaError_t launch(void (*kern)(P...), int64_t grid, int threads, size_t smem, v
   return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
 }
 
-// blocks of 256 threads for n threads' work, at most 16 per SM
-int64_t stride_grid(int64_t n) {
-  const int64_t need = (n + 255) / 256, most = 16ll * device_sm_count();
-  return need < most ? need : most;
+// a warp per tile and block
+int64_t pack_grid(const GroupShape &s) {
+  return (static_cast<int64_t>(s.tiles) * s.blocks + kPackWarps - 1) / kPackWarps;
+}
+
+template <typename T>
+w4a4_status launch_quantize(const uint16_t *W, const w4a4_group_weights_t *w, void *stream) {
+  const GroupShape s = shape_of(w->N, w->K, w->group);
+  auto kern = w->group == 32   ? group_quantize_kernel<T, 32>
+              : w->group == 64 ? group_quantize_kernel<T, 64>
+                               : group_quantize_kernel<T, 128>;
+  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, W, s, w->codes, w->scales));
+}
+
+template <typename T>
+w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *stream) {
+  const GroupShape s = shape_of(w->N, w->K, w->group);
+  auto kern = w->group == 32   ? group_dequantize_kernel<T, 32>
+              : w->group == 64 ? group_dequantize_kernel<T, 64>
+                               : group_dequantize_kernel<T, 128>;
+  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, w->codes, w->scales, s, W));
 }
 
 template <typename T, int GROUP, int RT, int NT>
@@ -432,10 +527,7 @@ w4a4_status w4a4_group_quantize(const uint16_t *W, const w4a4_group_weights_t *w
   if (st != W4A4_OK) return st;
   if (!W) return W4A4_ERR_ARG;
   if (!ptr_aligned16(W)) return W4A4_ERR_ALIGN;
-  const GroupShape s = shape_of(w->N, w->K, w->group);
-  const int64_t grid = stride_grid(static_cast<int64_t>(s.tiles) * 16 * s.blocks * 16);
-  return launch_status(launch((w->flags & W4A4_FLAG_FP16) ? group_quantize_kernel<Fp16> : group_quantize_kernel<Bf16>,
-                              grid, 256, 0, stream, W, s, w->codes, w->scales));
+  return (w->flags & W4A4_FLAG_FP16) ? launch_quantize<Fp16>(W, w, stream) : launch_quantize<Bf16>(W, w, stream);
 }
 
 w4a4_status w4a4_group_pack(const uint8_t *codes, const uint16_t *scales, const w4a4_group_weights_t *w,
@@ -446,8 +538,8 @@ w4a4_status w4a4_group_pack(const uint8_t *codes, const uint16_t *scales, const 
   if (!codes || !scales) return W4A4_ERR_ARG;
   if (!ptr_aligned16(codes) || !ptr_aligned16(scales)) return W4A4_ERR_ALIGN;
   const GroupShape s = shape_of(w->N, w->K, w->group);
-  const int64_t grid = stride_grid(static_cast<int64_t>(s.tiles) * 16 * s.blocks * 16);
-  return launch_status(launch(group_pack_kernel, grid, 256, 0, stream, codes, scales, s, w->codes, w->scales));
+  return launch_status(
+      launch(group_pack_kernel, pack_grid(s), 32 * kPackWarps, 0, stream, codes, scales, s, w->codes, w->scales));
 }
 
 w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *stream) {
@@ -456,11 +548,7 @@ w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, vo
   if (st != W4A4_OK) return st;
   if (!W) return W4A4_ERR_ARG;
   if (!ptr_aligned16(W)) return W4A4_ERR_ALIGN;
-  const GroupShape s = shape_of(w->N, w->K, w->group);
-  const int64_t grid = stride_grid(static_cast<int64_t>(s.N) * (s.K / 8));
-  return launch_status(
-      launch((w->flags & W4A4_FLAG_FP16) ? group_dequantize_kernel<Fp16> : group_dequantize_kernel<Bf16>, grid, 256, 0,
-             stream, w->codes, w->scales, s, W));
+  return (w->flags & W4A4_FLAG_FP16) ? launch_dequantize<Fp16>(w, W, stream) : launch_dequantize<Bf16>(w, W, stream);
 }
 
 w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weights_t *w, const uint16_t *bias,

@@ -38,44 +38,108 @@ struct AppendArgs {
   bool pairs;
 };
 
-// One block per token; thread by thread over its elements.
+// Two 16-byte pieces (8 elements each) of a head turned by 8 pairs of angles:
+// elements i of the first with i of the second, or neighbours within each.
 template <typename T>
-__global__ void __launch_bounds__(128) kv_append_kernel(AppendArgs a, unsigned int *__restrict__ status) {
+__device__ __forceinline__ void turn(uint4 &x, uint4 &y, const float (&c)[8], const float (&s)[8], bool pairs) {
+  uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
+  if (pairs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = T::lo(a[i]), a1 = T::hi(a[i]), b0 = T::lo(b[i]), b1 = T::hi(b[i]);
+      a[i] = T::pack(a0 * c[i] - a1 * s[i], a1 * c[i] + a0 * s[i]);
+      b[i] = T::pack(b0 * c[i + 4] - b1 * s[i + 4], b1 * c[i + 4] + b0 * s[i + 4]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a0 = T::lo(a[i]), a1 = T::hi(a[i]), b0 = T::lo(b[i]), b1 = T::hi(b[i]);
+      a[i] = T::pack(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
+      b[i] = T::pack(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
+    }
+  }
+  x = make_uint4(a[0], a[1], a[2], a[3]);
+  y = make_uint4(b[0], b[1], b[2], b[3]);
+}
+
+// ------------------------------------------------------------------- append
+//
+// Every byte of the new keys, values and queries is read and written once: bound by
+// HBM for prompts, by the chain position -> page -> store for a few tokens.  A warp
+// takes a token (or one of `parts` shares of its heads, where tokens are too few to
+// fill the GPU).  A lane keeps one unit of 16 elements for good, two pieces that turn
+// together, so the token's cosines and sines are read once into registers, and goes
+// over the heads in rounds of four whose loads are all in flight before the first
+// store, and before the page is known.  (One block per token, thread by
+// thread over its elements, took 67 us for 8 frames.)
+constexpr int kAppendWarps = 4;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kAppendWarps)
+    kv_append_kernel(AppendArgs a, int64_t T_, int parts, unsigned int *__restrict__ status) {
+  constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kRound = 4;  // units of a head, heads of a pass
   griddep_launch_dependents();
   griddep_wait();
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x & 31;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5);
+  const int64_t t = id / parts;
+  if (t >= T_) return;
+  const int part = static_cast<int>(id % parts);
+  const int u = lane % kUnits, hl = lane / kUnits;
   const int p = a.pos[t];
   if (p < 0) return;
   const int64_t s = a.seq ? a.seq[t] : t;
-  const int64_t turn = a.table_pos ? a.table_pos[t] : p;
+  const int64_t angle = a.table_pos ? a.table_pos[t] : p;
   const int entry = p / a.cache.page_size;
   int page = -1;
   if (s >= 0 && s < a.pages.n_seqs && entry < a.pages.max_pages) page = a.pages.table[s * a.pages.max_pages + entry];
-  if (page < 0 || page >= a.cache.n_pages || (a.rot_dim && (turn < 0 || turn >= a.n_table))) {
-    if (threadIdx.x == 0) atomicOr(status, W4A4_DEV_RANGE);
+  const bool turned = u < a.rot_dim / 16;
+  const bool in_table = a.rot_dim == 0 || (angle >= 0 && angle < a.n_table);
+  float c[8], sn[8];
+  if (turned && in_table) {
+    const float4 *row = reinterpret_cast<const float4 *>(a.table + angle * a.rot_dim + 8 * u);
+    const float4 *row2 = reinterpret_cast<const float4 *>(a.table + angle * a.rot_dim + a.rot_dim / 2 + 8 * u);
+    const float4 c0 = row[0], c1 = row[1], s0 = row2[0], s1 = row2[1];
+    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
+    sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+  }
+  // heads in the order keys, queries, values; the two pieces of this lane in each
+  const int Hk = a.cache.heads, Hq = a.q_heads, total = 2 * Hk + Hq;
+  const int halves = turned && !a.pairs;
+  const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? a.rot_dim / 2 + 8 * u : 16 * u + 8;
+  const int64_t row = page * a.cache.stride_page + (p - entry * a.cache.page_size) * a.cache.stride_token;
+  const bool ok = page >= 0 && page < a.cache.n_pages && in_table;
+  if (!ok) {
+    if (lane == 0) atomicOr(status, W4A4_DEV_RANGE);
     return;
   }
-  const int64_t row = page * a.cache.stride_page + (p % a.cache.page_size) * a.cache.stride_token;
-  const int D = a.head_dim, half = a.rot_dim / 2;
-  const float *tab = a.table + turn * a.rot_dim;
-  for (int u = threadIdx.x; u < a.cache.heads * D; u += 128)
-    a.cache.v[row + (u / D) * a.cache.stride_head + u % D] = a.v[t * a.v_stride + u];
-  // per head half turned pairs, then what is only copied
-  const int units = half + D - a.rot_dim;
-  for (int u = threadIdx.x; u < (a.cache.heads + a.q_heads) * units; u += 128) {
-    const int head = u / units, i = u % units;
-    const bool key = head < a.cache.heads;
-    const uint16_t *src = key ? a.k + t * a.k_stride + head * D : a.q + t * a.q_stride + (head - a.cache.heads) * D;
-    uint16_t *dst = key ? a.cache.k + row + head * a.cache.stride_head
-                        : a.q_out + (t * a.q_heads + (head - a.cache.heads)) * D;
-    if (i >= half) {
-      dst[i + half] = src[i + half];
-      continue;
+  for (int h0 = part * kHeads * kRound; h0 < total; h0 += parts * kHeads * kRound) {
+    uint4 x[kRound], y[kRound];
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const int h = h0 + i * kHeads + hl;
+      if (h < total) {
+        const bool value = h >= Hk + Hq;
+        const uint16_t *src = h < Hk ? a.k + t * a.k_stride + h * D
+                              : value ? a.v + t * a.v_stride + (h - Hk - Hq) * D
+                                      : a.q + t * a.q_stride + (h - Hk) * D;
+        x[i] = *reinterpret_cast<const uint4 *>(src + (value ? 16 * u : e0));
+        y[i] = *reinterpret_cast<const uint4 *>(src + (value ? 16 * u + 8 : e1));
+      }
     }
-    const int ia = a.pairs ? 2 * i : i, ib = a.pairs ? 2 * i + 1 : i + half;
-    const float x = T::to_f32(src[ia]), y = T::to_f32(src[ib]), c = tab[i], sn = tab[i + half];
-    dst[ia] = T::round(x * c - y * sn);
-    dst[ib] = T::round(y * c + x * sn);
+#pragma unroll
+    for (int i = 0; i < kRound; ++i) {
+      const int h = h0 + i * kHeads + hl;
+      if (h < total) {
+        const bool value = h >= Hk + Hq;
+        if (turned && !value) turn<T>(x[i], y[i], c, sn, a.pairs);
+        uint16_t *dst = h < Hk ? a.cache.k + row + h * a.cache.stride_head
+                        : value ? a.cache.v + row + (h - Hk - Hq) * a.cache.stride_head
+                                : a.q_out + (t * Hq + (h - Hk)) * D;
+        *reinterpret_cast<uint4 *>(dst + (value ? 16 * u : e0)) = x[i];
+        *reinterpret_cast<uint4 *>(dst + (value ? 16 * u + 8 : e1)) = y[i];
+      }
+    }
   }
 }
 
@@ -711,9 +775,17 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int6
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = launch_config(T, 128, 0, stream, &attr);
-  auto kern = (cache->flags & W4A4_FLAG_FP16) ? kv_append_kernel<Fp16> : kv_append_kernel<Bf16>;
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, a, status));
+  // shares of a token's heads (at most one per 4 passes of a warp) until there
+  // are 8 warps per SM
+  const int heads = 2 * a.cache.heads + a.q_heads, round = 4 * (32 / (D / 16)), most = (heads + round - 1) / round;
+  const int64_t want = (8ll * device_sm_count() + T - 1) / T;
+  const int parts = static_cast<int>(want < most ? want : most);
+  const cudaLaunchConfig_t cfg =
+      launch_config((T * parts + kAppendWarps - 1) / kAppendWarps, 32 * kAppendWarps, 0, stream, &attr);
+  const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0;
+  auto kern = D == 64 ? (fp16 ? kv_append_kernel<Fp16, 64> : kv_append_kernel<Bf16, 64>)
+                      : (fp16 ? kv_append_kernel<Fp16, 128> : kv_append_kernel<Bf16, 128>);
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, a, T, parts, status));
 }
 
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
