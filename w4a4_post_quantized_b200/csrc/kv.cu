@@ -553,84 +553,83 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
   if (tid == 0) a.joins[blockIdx.x] = join;
 }
 
-// One block per shared item and head: parts of blocks i..last, by 16-byte pieces.
+// One block per (block of the main kernel, head): where that block was the first of
+// a shared item, the item's parts are joined, those of blocks first..last.  A lane takes 4 dims
+// of every kGroups-th part with its own running maximum and sum, 8 parts in flight: after
+// the wait three dependent reads remain.  Blocks without an item leave at once; all
+// fit on the GPU together.  (A list of the shared items made by each block first, then a
+// pass for the weights and one for the outputs, took 11 to 24 us.)
+constexpr int kJoinThreads = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv_join_kernel(AttendArgs a, int blocks) {
-  constexpr int kPart = D + 4, kLanes = D / 4, kGroups = 256 / kLanes;
-  __shared__ float weight[kMaxBlocks];
-  __shared__ float red[16];
-  __shared__ int jobs[kMaxBlocks];
-  __shared__ int n_jobs;
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs a) {
+  constexpr int kPart = D + 4, kLanes = D / 4, kGroups = kJoinThreads / kLanes, kFlight = 8;
   __shared__ float4 box[kGroups][kLanes];
+  __shared__ float2 stats[kGroups];
   griddep_launch_dependents();
   griddep_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) {  // the blocks that begin a shared item, in order
-    int n = 0;
-    for (int i = 0; i < blocks; i += 32) {
-      const bool lead = i + lane < blocks && a.joins[i + lane].x >= 0;
-      const uint32_t all = __ballot_sync(0xffffffffu, lead);
-      if (lead) jobs[n + __popc(all & ((1u << lane) - 1u))] = i + lane;
-      n += __popc(all);
-    }
-    if (lane == 0) n_jobs = n;
-  }
-  __syncthreads();
-  for (int job = blockIdx.x; job < n_jobs * a.chunk; job += gridDim.x) {
-    const int lead = jobs[job / a.chunk], h = job % a.chunk;
-    const int4 j = a.joins[lead];
-    const int kvh = j.y / a.chunks, h0 = (j.y % a.chunks) * a.chunk;
-    if (h >= min(a.chunk, a.group - h0)) continue;
-    const int parts = j.w - lead + 1;
-    auto part = [&](int i) {
-      return a.part + ((static_cast<int64_t>(lead + i) * 2 + (i == 0 ? j.z : 0)) * a.chunk + h) * kPart;
-    };
-    float top = -INFINITY;
-    for (int i = tid; i < parts; i += 256) {
-      weight[i] = part(i)[D];
-      top = fmaxf(top, weight[i]);
-    }
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[warp] = top;
-    __syncthreads();
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, red[w]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    float sum = 0.0f;
-    for (int i = tid; i < parts; i += 256) {
-      const float f = exp2f(weight[i] - base);
-      sum = fmaf(f, part(i)[D + 1], sum);
-      weight[i] = f;
-    }
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[8 + warp] = sum;
-    __syncthreads();
-    sum = 0.0f;
-    for (int w = 0; w < 8; ++w) sum += red[8 + w];
-    const int g = tid / kLanes, d = 4 * (tid % kLanes);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = g; i < parts; i += kGroups) {
-      const float f = weight[i];
-      const float4 v = *reinterpret_cast<const float4 *>(part(i) + d);
-      o.x = fmaf(f, v.x, o.x);
-      o.y = fmaf(f, v.y, o.y);
-      o.z = fmaf(f, v.z, o.z);
-      o.w = fmaf(f, v.w, o.w);
-    }
-    box[g][tid % kLanes] = o;
-    __syncthreads();
-    if (g == 0) {
-      for (int i = 1; i < kGroups; ++i) {
-        const float4 v = box[i][tid];
-        o.x += v.x;
-        o.y += v.y;
-        o.z += v.z;
-        o.w += v.w;
+  const int lead = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  const int4 j = a.joins[lead];
+  if (j.x < 0) return;
+  const int kvh = j.y / a.chunks, h0 = (j.y % a.chunks) * a.chunk;
+  if (h >= min(a.chunk, a.group - h0)) return;
+  const int parts = j.w - lead + 1, g = tid / kLanes, d = 4 * (tid % kLanes);
+  // this item's part is its first block's slot j.z, every later block's slot 0
+  const float *first = a.part + ((static_cast<int64_t>(lead) * 2 + j.z) * a.chunk + h) * kPart;
+  const float *later = a.part + (static_cast<int64_t>(lead) * 2 * a.chunk + h) * kPart;
+  float m = -INFINITY, sum = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int i0 = g; i0 < parts; i0 += kGroups * kFlight) {
+    float4 v[kFlight];
+    float2 ml[kFlight];
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const int i = i0 + f * kGroups;
+      v[f] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      ml[f] = make_float2(-INFINITY, 0.0f);
+      if (i < parts) {
+        const float *p = i == 0 ? first : later + static_cast<int64_t>(i) * 2 * a.chunk * kPart;
+        v[f] = *reinterpret_cast<const float4 *>(p + d);
+        ml[f] = *reinterpret_cast<const float2 *>(p + D);
       }
-      write_out<T, D>(a, j.x, kvh * a.group + h0 + h, d, o, base, sum);
     }
-    __syncthreads();
+    float top = m;
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) top = fmaxf(top, ml[f].x);
+    const float base = top == -INFINITY ? 0.0f : top, keep = exp2f(m - base);
+    m = top;
+    sum *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
+#pragma unroll
+    for (int f = 0; f < kFlight; ++f) {
+      const float w = exp2f(ml[f].x - base);
+      sum = fmaf(w, ml[f].y, sum);
+      o.x = fmaf(w, v[f].x, o.x);
+      o.y = fmaf(w, v[f].y, o.y);
+      o.z = fmaf(w, v[f].z, o.z);
+      o.w = fmaf(w, v[f].w, o.w);
+    }
   }
+  box[g][tid % kLanes] = o;
+  if (tid % kLanes == 0) stats[g] = make_float2(m, sum);
+  __syncthreads();
+  if (g != 0) return;
+#pragma unroll
+  for (int i = 1; i < kGroups; ++i) m = fmaxf(m, stats[i].x);
+  const float base = m == -INFINITY ? 0.0f : m;
+  sum = 0.0f;
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    const float w = exp2f(stats[i].x - base);
+    const float4 v = box[i][tid];
+    sum = fmaf(w, stats[i].y, sum);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  write_out<T, D>(a, j.x, kvh * a.group + h0 + h, d, o, base, sum);
 }
 
 w4a4_status check_cache(const w4a4_kv_cache_t *c, Cache *out) {
@@ -702,9 +701,9 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
   if (e != cudaSuccess || grid == 1) return launch_status(e);
-  const int64_t jobs = grid * a.chunk, most = 2ll * device_sm_count();
-  cfg = launch_config(jobs < most ? jobs : most, 256, 0, stream, &attr);
-  return launch_status(cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a, static_cast<int>(grid)));
+  cfg = launch_config(grid, kJoinThreads, 0, stream, &attr);
+  cfg.gridDim.y = static_cast<unsigned>(a.chunk);
+  return launch_status(cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a));
 }
 
 }  // namespace

@@ -11,7 +11,6 @@ Calls are asynchronous on the given stream (default: torch's current stream).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -412,21 +411,29 @@ def tq_decode_dense(codes: torch.Tensor, norms: torch.Tensor, pit_hi: torch.Tens
 
 
 # ------------------------------------------- single-token operators (include/decode.h)
-def _enter(dev: torch.device, stream):
-    """The stream to launch on, and a context that makes `dev` current (and
-    `stream` the allocating one) where it is not; None when nothing has to change."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-        return stream.cuda_stream, torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.current_stream(dev).cuda_stream, torch.cuda.device(dev)
-    return torch.cuda.current_stream().cuda_stream, None
+def _here(dev: torch.device, stream):
+    """The raw current stream when the call can run as things stand: on the
+    current device, on torch's current stream.  Otherwise None, and the call is made
+    again inside _elsewhere.  (torch.cuda.current_stream() builds an object, 3 us of a
+    call whose kernel takes 2; the raw handle costs 0.1.)"""
+    if stream is None and dev.index == torch.cuda.current_device():
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return None
+
+
+def _elsewhere(dev: torch.device, stream):
+    """A context in which `dev` is current and `stream` (where given) torch's
+    stream, so that what a call allocates belongs to the stream it is used on."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _need(t: torch.Tensor, name: str, dtype, dev, shape) -> int:
     """The address of a contiguous tensor of that type, device and shape."""
-    if t.dtype != dtype or t.device != dev or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: need a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -477,22 +484,24 @@ class GroupWeights:
         self.storage = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self.device = self.storage.device
         self.struct = GroupWeightsT()
-        _check(_group_bind(_ptr(self.storage), nbytes, N, K, group, flags, ctypes.byref(self.struct)),
-               "w4a4_group_bind")
+        self.ref = ctypes.byref(self.struct)
+        _check(_group_bind(_ptr(self.storage), nbytes, N, K, group, flags, self.ref), "w4a4_group_bind")
 
 
 def w4a4_group_quantize(W: torch.Tensor, group: int = 128, out: GroupWeights | None = None,
                         stream=None) -> GroupWeights:
     """W [N, K] bf16 or fp16 -> 4-bit codes with one step per `group` inputs."""
     dev = _cuda_device(W, "W")
-    N, K = W.shape
-    st, ctx = _enter(dev, stream)
-    with ctx or contextlib.nullcontext():
-        out = out if out is not None else GroupWeights(N, K, group, W.dtype, dev)
-        if out.group != group or out.device != dev:
-            raise ValueError(f"out has groups of {out.group} on {out.device}, asked for {group} on {dev}")
-        w = _need(W, "W", out.dtype, dev, (out.N, out.K))
-        _check(_group_quantize(w, ctypes.byref(out.struct), st), "w4a4_group_quantize")
+    st = _here(dev, stream)
+    if st is None:
+        with _elsewhere(dev, stream):
+            return w4a4_group_quantize(W, group, out)
+    if out is None:
+        out = GroupWeights(W.shape[0], W.shape[1], group, W.dtype, dev)
+    if out.group != group:
+        raise ValueError(f"out has groups of {out.group}, asked for {group}")
+    _check(_group_quantize(_need(W, "W", out.dtype, out.device, (out.N, out.K)), out.ref, st),
+           "w4a4_group_quantize")
     return out
 
 
@@ -501,40 +510,50 @@ def w4a4_group_pack(codes: torch.Tensor, scales: torch.Tensor, out: GroupWeights
     """codes [N, K/2] uint8 (element 2i in the low nibble) and scales [N,
     K/group] made elsewhere -> GroupWeights."""
     dev = _cuda_device(codes, "codes")
-    N, K = codes.shape[0], 2 * codes.shape[1]
-    st, ctx = _enter(dev, stream)
-    with ctx or contextlib.nullcontext():
-        if out is None:
-            if scales.dim() != 2 or scales.shape[1] == 0 or K % scales.shape[1]:
-                raise ValueError(f"scales {tuple(scales.shape)} do not divide {K} inputs into groups")
-            out = GroupWeights(N, K, K // scales.shape[1], scales.dtype, dev)
-        c = _need(codes, "codes", torch.uint8, out.device, (out.N, out.K // 2))
-        s = _need(scales, "scales", out.dtype, out.device, (out.N, out.K // out.group))
-        _check(_group_pack(c, s, ctypes.byref(out.struct), st), "w4a4_group_pack")
+    st = _here(dev, stream)
+    if st is None:
+        with _elsewhere(dev, stream):
+            return w4a4_group_pack(codes, scales, out)
+    if out is None:
+        N, K = codes.shape[0], 2 * codes.shape[1]
+        if scales.dim() != 2 or scales.shape[1] == 0 or K % scales.shape[1]:
+            raise ValueError(f"scales {tuple(scales.shape)} do not divide {K} inputs into groups")
+        out = GroupWeights(N, K, K // scales.shape[1], scales.dtype, dev)
+    c = _need(codes, "codes", torch.uint8, out.device, (out.N, out.K // 2))
+    s = _need(scales, "scales", out.dtype, out.device, (out.N, out.K // out.group))
+    _check(_group_pack(c, s, out.ref, st), "w4a4_group_pack")
     return out
 
 
 def w4a4_group_dequantize(w: GroupWeights, W=None, stream=None) -> torch.Tensor:
     """The weights [N, K] that the codes and steps stand for."""
-    st, ctx = _enter(w.device, stream)
-    with ctx or contextlib.nullcontext():
-        W = W if W is not None else torch.empty((w.N, w.K), dtype=w.dtype, device=w.device)
-        p = _need(W, "W", w.dtype, w.device, (w.N, w.K))
-        _check(_group_dequantize(ctypes.byref(w.struct), p, st), "w4a4_group_dequantize")
+    st = _here(w.device, stream)
+    if st is None:
+        with _elsewhere(w.device, stream):
+            return w4a4_group_dequantize(w, W)
+    if W is None:
+        W = torch.empty((w.N, w.K), dtype=w.dtype, device=w.device)
+    _check(_group_dequantize(w.ref, _need(W, "W", w.dtype, w.device, (w.N, w.K)), st), "w4a4_group_dequantize")
     return W
 
 
 def w4a4_group_gemv(X: torch.Tensor, w: GroupWeights, bias=None, Y=None, flags: int = 0,
                     stream=None) -> torch.Tensor:
     """Y [M, N] = X [M, K] W^T + bias for up to 16 tokens."""
+    dev, dt = w.device, w.dtype
+    st = _here(dev, stream)
+    if st is None:
+        with _elsewhere(dev, stream):
+            return w4a4_group_gemv(X, w, bias, Y, flags)
     M = X.shape[0]
-    st, ctx = _enter(w.device, stream)
-    with ctx or contextlib.nullcontext():
-        x = _need(X, "X", w.dtype, w.device, (M, w.K))
-        b = None if bias is None else _need(bias, "bias", w.dtype, w.device, (w.N,))
-        Y = Y if Y is not None else torch.empty((M, w.N), dtype=w.dtype, device=w.device)
-        y = _need(Y, "Y", w.dtype, w.device, (M, w.N))
-        _check(_group_gemv(x, M, ctypes.byref(w.struct), b, y, flags, st), "w4a4_group_gemv")
+    x = _need(X, "X", dt, dev, (M, w.K))
+    if Y is None:
+        Y = X.new_empty((M, w.N))
+        y = Y.data_ptr()
+    else:
+        y = _need(Y, "Y", dt, dev, (M, w.N))
+    _check(_group_gemv(x, M, w.ref, None if bias is None else _need(bias, "bias", dt, dev, (w.N,)), y, flags, st),
+           "w4a4_group_gemv")
     return Y
 
 
@@ -563,6 +582,7 @@ class KVCache:
         # a dimension of one element has no stride of its own
         sp, ss, sh = (k.stride(i) if k.shape[i] > 1 else 0 for i in range(3))
         self.struct = KVCacheT(k.data_ptr(), v.data_ptr(), P, S, H, D, _half_flag(k.dtype), sp, ss, sh)
+        self.ref = ctypes.byref(self.struct)
 
 
 def w4a4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pages: torch.Tensor, pos: torch.Tensor,
@@ -571,33 +591,37 @@ def w4a4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pages: torc
     seq [T] (default: token t is sequence t), whose pages are the row of pages [n_seqs, max_pages].  Keys, and
     q [T, q_heads, head_dim], are rotated by row table_pos[t] (default pos[t]) of table [n, rot_dim] fp32.
     Returns the rotated q (None without q)."""
-    T = k.shape[0]
     dev, dt = cache.device, cache.dtype
-    st, ctx = _enter(dev, stream)
-    with ctx or contextlib.nullcontext():
-        kp, ks = _rows(k, "k", dt, dev, (T, cache.n_heads, cache.head_dim))
-        vp, vs = _rows(v, "v", dt, dev, (T, cache.n_heads, cache.head_dim))
-        qp = qs = op = None
-        hq = 0
-        if q is not None:
-            hq = q.shape[1]
-            qp, qs = _rows(q, "q", dt, dev, (T, hq, cache.head_dim))
-            q_out = q_out if q_out is not None else torch.empty((T, hq, cache.head_dim), dtype=dt, device=dev)
-            op = _need(q_out, "q_out", dt, dev, (T, hq, cache.head_dim))
-        n_seqs, max_pages = pages.shape
-        n_table = rot = 0
-        tp = None
-        if table is not None:
-            n_table, rot = table.shape
-            tp = _need(table, "table", torch.float32, dev, (n_table, rot))
-        if seq is None and T > n_seqs:
-            raise ValueError(f"{T} tokens for {n_seqs} sequences need seq")
-        _check(_kv_append(ctypes.byref(cache.struct), kp, ks, vp, vs, qp, qs or 0, hq, op, T,
-                          _need(pages, "pages", torch.int32, dev, (n_seqs, max_pages)), n_seqs, max_pages,
-                          None if seq is None else _need(seq, "seq", torch.int32, dev, (T,)),
-                          _need(pos, "pos", torch.int32, dev, (T,)), tp, n_table, rot,
-                          None if table_pos is None else _need(table_pos, "table_pos", torch.int32, dev, (T,)),
-                          flags, st), "w4a4_kv_append")
+    st = _here(dev, stream)
+    if st is None:
+        with _elsewhere(dev, stream):
+            return w4a4_kv_append(cache, k, v, pages, pos, q, q_out, table, table_pos, seq, flags)
+    T = k.shape[0]
+    kp, ks = _rows(k, "k", dt, dev, (T, cache.n_heads, cache.head_dim))
+    vp, vs = _rows(v, "v", dt, dev, (T, cache.n_heads, cache.head_dim))
+    qp = op = tp = None
+    qs = hq = n_table = rot = 0
+    if q is not None:
+        hq = q.shape[1]
+        shape = (T, hq, cache.head_dim)
+        qp, qs = _rows(q, "q", dt, dev, shape)
+        if q_out is None:
+            q_out = q.new_empty(shape)
+            op = q_out.data_ptr()
+        else:
+            op = _need(q_out, "q_out", dt, dev, shape)
+    n_seqs, max_pages = pages.shape
+    if table is not None:
+        n_table, rot = table.shape
+        tp = _need(table, "table", torch.float32, dev, (n_table, rot))
+    if seq is None and T > n_seqs:
+        raise ValueError(f"{T} tokens for {n_seqs} sequences need seq")
+    _check(_kv_append(cache.ref, kp, ks, vp, vs, qp, qs, hq, op, T,
+                      _need(pages, "pages", torch.int32, dev, (n_seqs, max_pages)), n_seqs, max_pages,
+                      None if seq is None else _need(seq, "seq", torch.int32, dev, (T,)),
+                      _need(pos, "pos", torch.int32, dev, (T,)), tp, n_table, rot,
+                      None if table_pos is None else _need(table_pos, "table_pos", torch.int32, dev, (T,)),
+                      flags, st), "w4a4_kv_append")
     return None if q is None else q_out
 
 
@@ -610,23 +634,26 @@ def w4a4_kv_attend(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: t
     """One new token per sequence: q [n_seqs, q_heads, head_dim] against the lens [n_seqs] (int32) cached
     tokens of its sequence, the last `window` of them where window > 0.  scale: 1 / sqrt(head_dim) by
     default.  lse [n_seqs, q_heads] fp32 receives the logarithm of the sum of exponentials."""
-    B, Hq, D = q.shape
     dev, dt = cache.device, cache.dtype
-    st, ctx = _enter(dev, stream)
-    with ctx or contextlib.nullcontext():
-        qp, qs = _rows(q, "q", dt, dev, (B, Hq, cache.head_dim))
-        max_pages = pages.shape[1]
-        out = out if out is not None else torch.empty((B, Hq, D), dtype=dt, device=dev)
-        need = w4a4_kv_attend_workspace_bytes(B, Hq, cache.n_heads, D)
-        if workspace is None:
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-        _check(_kv_attend(qp, qs, Hq, ctypes.byref(cache.struct),
-                          _need(pages, "pages", torch.int32, dev, (B, max_pages)), B, max_pages,
-                          _need(lens, "lens", torch.int32, dev, (B,)), D ** -0.5 if scale is None else scale,
-                          window, _need(out, "out", dt, dev, (B, Hq, D)),
-                          None if lse is None else _need(lse, "lse", torch.float32, dev, (B, Hq)),
-                          workspace.data_ptr(), workspace.numel() * workspace.element_size(), st),
-               "w4a4_kv_attend")
+    st = _here(dev, stream)
+    if st is None:
+        with _elsewhere(dev, stream):
+            return w4a4_kv_attend(q, cache, pages, lens, scale, window, out, lse, workspace)
+    B, Hq, D = q.shape
+    qp, qs = _rows(q, "q", dt, dev, (B, Hq, cache.head_dim))
+    max_pages = pages.shape[1]
+    if out is None:
+        out = q.new_empty((B, Hq, D))
+        op = out.data_ptr()
+    else:
+        op = _need(out, "out", dt, dev, (B, Hq, D))
+    if workspace is None:
+        need = _kv_attend_ws(B, Hq, cache.n_heads, D)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: need a contiguous tensor on {dev}")
+    _check(_kv_attend(qp, qs, Hq, cache.ref, _need(pages, "pages", torch.int32, dev, (B, max_pages)), B, max_pages,
+                      _need(lens, "lens", torch.int32, dev, (B,)), D ** -0.5 if scale is None else scale, window, op,
+                      None if lse is None else _need(lse, "lse", torch.float32, dev, (B, Hq)),
+                      workspace.data_ptr(), workspace.nbytes, st), "w4a4_kv_attend")
     return out
