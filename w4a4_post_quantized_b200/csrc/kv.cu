@@ -179,6 +179,8 @@ constexpr int kTile = 64;            // tokens of a block's tile: 16 per warp
 constexpr int kMaxBlocks = 640;      // partial results in the workspace: 2 per block
 constexpr int kChunk = 16;           // most query heads of a block's item
 
+constexpr int attend_stages(int D) { return D == 64 ? 5 : 2; }
+
 struct AttendArgs {
   Cache cache;
   Pages pages;
@@ -242,6 +244,12 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// a / b without the cost of a 64-bit division where 32 bits do
+__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // Four output elements from d on of query head h, and at d = 0 its lse.
 template <typename T, int D>
 __device__ __forceinline__ void write_out(const AttendArgs &a, int b, int h, int d, float4 o, float base, float sum) {
@@ -253,7 +261,7 @@ __device__ __forceinline__ void write_out(const AttendArgs &a, int b, int h, int
 
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs a, unsigned int *__restrict__ status) {
-  constexpr int kStages = D == 64 ? 4 : 3;
+  constexpr int kStages = attend_stages(D);
   constexpr int kRow = 2 * D;                 // bytes of a row
   constexpr int kStage = 2 * 16 * kRow;       // 16 keys, 16 values
   constexpr int kPieces = D / 8;
@@ -306,7 +314,10 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
     if (tid == 0) a.joins[blockIdx.x].x = -1;
     return;
   }
-  const int64_t begin = blockIdx.x * total / blocks, stop = (blockIdx.x + 1) * total / blocks;
+  // equal shares, the first `more` blocks one tile more
+  const int64_t share = div_small(total, blocks), more = total - share * blocks;
+  const int64_t begin = blockIdx.x * share + min(static_cast<int64_t>(blockIdx.x), more);
+  const int64_t stop = begin + share + (blockIdx.x < more ? 1 : 0);
   if (upto - mine <= begin && begin < upto) {
     int64_t at = upto - mine;
     int b = tid * run;
@@ -335,8 +346,8 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
       ++b;
       continue;
     }
-    const int item = static_cast<int>((u - seq_at) / tiles);
-    const int t0 = static_cast<int>((u - seq_at) % tiles);
+    const int item = static_cast<int>(div_small(u - seq_at, tiles));
+    const int t0 = static_cast<int>(u - seq_at - static_cast<int64_t>(item) * tiles);
     const int t1 = static_cast<int>(min(static_cast<int64_t>(tiles), t0 + (stop - u)));
     const int kvh = item / a.chunks;
     const int h0 = (item % a.chunks) * a.chunk;            // first head of the chunk, in its group
@@ -542,9 +553,10 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
       }
     }
     if (!whole && t0 == 0) {
-      // the block that holds the item's last tile: block i's share ends at (i + 1) total / blocks
-      const int64_t last = u + tiles - 1;
-      join = make_int4(b, item, slot, static_cast<int>(((last + 1) * blocks - 1) / total));
+      // the block that holds the item's last tile
+      const int64_t last = u + tiles - 1, wide = more * (share + 1);
+      join = make_int4(b, item, slot,
+                       static_cast<int>(last < wide ? div_small(last, share + 1) : more + div_small(last - wide, share)));
     }
     __syncthreads();                                        // before the rings are filled again
     u += t1 - t0;
@@ -676,7 +688,7 @@ size_t part_bytes(int group, int D) {
 
 template <typename T, int D, int NT>
 w4a4_status launch_attend(AttendArgs &a, void *stream) {
-  constexpr int kStages = D == 64 ? 4 : 3;
+  constexpr int kStages = attend_stages(D);
   constexpr int kRing = kAttendWarps * kStages * 2 * 16 * 2 * D, kBox = kAttendWarps * 8 * NT * (D + 4) * 4;
   constexpr int kSmem = kRing > kBox ? kRing : kBox;
   static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
