@@ -13,6 +13,13 @@
 namespace w4a4 {
 namespace {
 
+// (a & b) ^ c in one instruction
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 struct Bf16 {
   static __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   // element 0 of a packed pair in the low half
@@ -38,7 +45,7 @@ struct Bf16 {
   static __device__ __forceinline__ void codes(uint32_t w, uint32_t (&o)[4]) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
-      const uint32_t v = ((w >> (4 * p)) & 0x000F000Fu) ^ 0x43084308u;
+      const uint32_t v = and_xor(w >> (4 * p), 0x000F000Fu, 0x43084308u);
       asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(o[p]) : "r"(v), "r"(0x43084308u));
     }
   }
@@ -77,10 +84,10 @@ struct Fp16 {
 #pragma unroll
     for (int p = 0; p < 4; p += 2) {
       const uint32_t v = w >> (4 * p);
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[p]) : "r"((v & 0x000F000Fu) ^ 0x64086408u), "r"(0x64086408u));
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(o[p]) : "r"(and_xor(v, 0x000F000Fu, 0x64086408u)), "r"(0x64086408u));
       // (2^10 + 16 u) / 16 - 72
       asm("fma.rn.f16x2 %0, %1, %2, %3;"
-          : "=r"(o[p + 1]) : "r"((v & 0x00F000F0u) ^ 0x64806480u), "r"(0x2C002C00u), "r"(0xD480D480u));
+          : "=r"(o[p + 1]) : "r"(and_xor(v, 0x00F000F0u, 0x64806480u)), "r"(0x2C002C00u), "r"(0xD480D480u));
     }
   }
   // d (16 x 8) += A (16 x 16) B (16 x 8), fp32 sums

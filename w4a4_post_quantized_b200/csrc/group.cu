@@ -271,41 +271,68 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
   const int kb1 = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks / kGemvWarps);
   const int row_groups = (s.tiles + RT - 1) / RT;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  const int64_t tile_codes = static_cast<int64_t>(s.blocks) * 1024;
+  const int64_t tile_steps = static_cast<int64_t>(s.blocks) * 8 * kScaleRow;
 
-  auto tile_at = [&](int rg, int t, int kb) {
-    return static_cast<int64_t>(min(rg * RT + t, s.tiles - 1)) * s.blocks + kb;
-  };
+  // The copy stream: row groups blockIdx.x, + gridDim.x, ..., of each the warp's
+  // blocks of inputs.  An odd last tile is its own second.
+  int copy_rg = blockIdx.x, copy_left = kb1 - kb0;
+  uint32_t copy_dst = ring;
+  const uint8_t *from = a.codes + copy_rg * RT * tile_codes + kb0 * 1024 + 16 * lane;
+  const uint8_t *steps_from = reinterpret_cast<const uint8_t *>(a.scales) + copy_rg * RT * tile_steps +
+                              (kb0 * 8 + (lane & 7)) * kScaleRow;
+  int64_t second_codes = copy_rg * RT + 1 < s.tiles ? tile_codes : 0, second_steps = second_codes ? tile_steps : 0;
   griddep_launch_dependents();
-  for (int kb = kb0; kb < min(kb1, kb0 + kStages); ++kb)
-#pragma unroll
-    for (int t = 0; t < RT; ++t)
-      if (lane < 8) prefetch_l2(a.codes + tile_at(blockIdx.x, t, kb) * 1024 + 128 * lane);
+  if (lane < 8)
+    for (int kb = kb0; kb < min(kb1, kb0 + kStages); ++kb) {
+      const uint8_t *p = from + (kb - kb0) * 1024 + 112 * lane;  // 128 bytes a lane
+      prefetch_l2(p);
+      if (RT == 2) prefetch_l2(p + second_codes);
+    }
   griddep_wait();
-
-  // the copy stream: (row group, block of inputs) pairs in order
-  int copy_rg = blockIdx.x, copy_kb = kb0, copy_stage = 0;
   auto fill = [&]() {
-    if (kb0 < kb1 && copy_rg < row_groups) {
-      const uint32_t dst = ring + copy_stage * kStage;
+    if (copy_rg < row_groups && kb0 < kb1) {
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const int64_t at = tile_at(copy_rg, t, copy_kb);
-        copy16(dst + t * 1024 + 16 * lane, a.codes + at * 1024 + 16 * lane);
-        copy16(dst + t * 1024 + 512 + 16 * lane, a.codes + at * 1024 + 512 + 16 * lane);
+        const uint8_t *f = t ? from + second_codes : from;
+        copy16(copy_dst + t * 1024 + 16 * lane, f);
+        copy16(copy_dst + t * 1024 + 512 + 16 * lane, f + 512);
         if (lane < 8)
-          copy_small<kScaleRow>(dst + RT * 1024 + (t * 8 + lane) * kScaleRow,
-                                a.scales + (at * 8 + lane) * (kScaleRow / 2));
+          copy_small<kScaleRow>(copy_dst + RT * 1024 + (t * 8 + lane) * kScaleRow,
+                                t ? steps_from + second_steps : steps_from);
       }
-      copy_stage = copy_stage == kStages - 1 ? 0 : copy_stage + 1;
-      if (++copy_kb == kb1) {
-        copy_kb = kb0;
+      copy_dst = copy_dst == ring + (kStages - 1) * kStage ? ring : copy_dst + kStage;
+      from += 1024;
+      steps_from += 8 * kScaleRow;
+      if (--copy_left == 0) {
+        copy_left = kb1 - kb0;
         copy_rg += gridDim.x;
+        from += gridDim.x * (RT * tile_codes) - copy_left * 1024;
+        steps_from += gridDim.x * (RT * tile_steps) - copy_left * (8 * kScaleRow);
+        if (copy_rg * RT + 1 >= s.tiles) second_codes = second_steps = 0;
       }
     }
     copy_commit();
   };
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) fill();
+
+  // Tokens r and r + 8 as the B operand; columns behind the last token repeat it
+  // (their sums are not used).
+  const uint16_t *x_row[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) x_row[n] = a.X + static_cast<int64_t>(min(8 * n + r, a.M - 1)) * s.K + 8 * c;
+  auto load_x = [&](uint4 (&x)[NT][4], int kb) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[n][j] = kb * kBlockK + 32 * j < s.K
+                      ? __ldg(reinterpret_cast<const uint4 *>(x_row[n] + kb * kBlockK + 32 * j))
+                      : make_uint4(0u, 0u, 0u, 0u);
+  };
+  uint4 x[NT][4];
+  if (kb0 < kb1) load_x(x, kb0);
 
   int stage = 0, parity = 0;
   for (int rg = blockIdx.x; rg < row_groups; rg += gridDim.x, parity ^= 1) {
@@ -317,21 +344,13 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
 #pragma unroll
         for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
     for (int kb = kb0; kb < kb1; ++kb) {
-      // tokens r, r + 8 as the B operand: inputs 32 j + 8 c .. + 7 of the block
-      uint4 x[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k = kb * kBlockK + 32 * j + 8 * c;
-          x[n][j] = make_uint4(0u, 0u, 0u, 0u);
-          if (8 * n + r < a.M && k < s.K)
-            x[n][j] = __ldg(reinterpret_cast<const uint4 *>(a.X + static_cast<int64_t>(8 * n + r) * s.K + k));
-        }
       copy_wait<kStages - 2>();
       __syncwarp();
       fill();
       const uint32_t base = ring + stage * kStage;
+      // the next block's tokens; after the last block the first one's, for the next row group
+      uint4 ahead[NT][4];
+      load_x(ahead, kb + 1 < kb1 ? kb + 1 : kb0);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         uint4 w0, w1;
@@ -374,6 +393,10 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
         }
       }
       stage = stage == kStages - 1 ? 0 : stage + 1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = ahead[n][j];
     }
     // the eighths meet; two sets of sums, so one barrier per row group is enough
 #pragma unroll

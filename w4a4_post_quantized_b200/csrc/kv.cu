@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
       }
     };
     int ahead = warp;                                       // next piece to fill
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < kStages - 1; ++s) {
       if (ahead < subs) fill(s, row_of(ahead));
       copy_commit();
@@ -712,7 +712,8 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
-  if (e != cudaSuccess || grid == 1) return launch_status(e);
+  // one block, or items of one tile: nothing is shared
+  if (e != cudaSuccess || grid == 1 || tiles <= 1) return launch_status(e);
   cfg = launch_config(grid, kJoinThreads, 0, stream, &attr);
   cfg.gridDim.y = static_cast<unsigned>(a.chunk);
   return launch_status(cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a));

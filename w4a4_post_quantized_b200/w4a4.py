@@ -441,13 +441,14 @@ def _need(t: torch.Tensor, name: str, dtype, dev, shape) -> int:
 
 def _rows(t: torch.Tensor, name: str, dtype, dev, shape) -> tuple[int, int]:
     """Address and row stride of a tensor [T, heads, head_dim] whose rows are dense."""
-    if t.dtype != dtype or t.device != dev or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
         raise ValueError(f"{name}: need {dtype} of shape {tuple(shape)} on {dev}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     T, H, D = shape
-    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and H > 1):
+    row, head, one = t.stride()
+    if one != 1 or (head != D and H > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous, strides are {t.stride()}")
-    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), row if T > 1 else H * D
 
 
 def _half_flag(dtype) -> int:
