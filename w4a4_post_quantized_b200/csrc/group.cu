@@ -227,7 +227,8 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    to be brought into L2: those do not depend on that kernel, and where they do
 //    (a quantization right before) L2 is where the new values appear.
 
-constexpr int kGemvWarps = 8;
+constexpr int kGemvWarps = 16;
+constexpr int gemv_stages(int RT) { return RT == 1 ? 6 : 3; }
 
 struct GemvArgs {
   const uint16_t *X;
@@ -238,6 +239,7 @@ struct GemvArgs {
   const uint16_t *bias;
   uint16_t *Y;
   bool gelu;
+  int team;  // warps that share the inputs of a row group: 1, 2, 4, 8 or 16
 };
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -256,34 +258,39 @@ __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefe
 
 // GROUP inputs per step, RT tiles of 16 rows per block, NT times 8 tokens.
 template <typename T, int GROUP, int RT, int NT>
-__global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs a) {
+__global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs a) {
   constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
   constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
   constexpr int kStage = RT * (1024 + 8 * kScaleRow);
-  constexpr int kStages = RT == 1 ? 8 : 5;
+  constexpr int kStages = gemv_stages(RT);
   constexpr int kRows = 16 * RT, kCols = 8 * NT;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float sums[2][kGemvWarps][kCols][kRows + 1];
+  typedef float Sums[kGemvWarps][kCols][kRows + 1];
+  Sums *sums = reinterpret_cast<Sums *>(smem + kGemvWarps * kStages * kStage);  // [2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const GroupShape &s = a.s;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(warp) * s.blocks / kGemvWarps);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks / kGemvWarps);
+  // this warp's part of the inputs, and its team's first row group and stride: teams of one
+  // number over all blocks come first, so that SMs get equally many
+  const int part = warp % a.team, first_rg = blockIdx.x + gridDim.x * (warp / a.team);
+  const int rg_step = gridDim.x * (kGemvWarps / a.team);
+  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * s.blocks / a.team);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * s.blocks / a.team);
   const int row_groups = (s.tiles + RT - 1) / RT;
   const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
   const int64_t tile_codes = static_cast<int64_t>(s.blocks) * 1024;
   const int64_t tile_steps = static_cast<int64_t>(s.blocks) * 8 * kScaleRow;
 
-  // The copy stream: row groups blockIdx.x, + gridDim.x, ..., of each the warp's
-  // blocks of inputs.  An odd last tile is its own second.
-  int copy_rg = blockIdx.x, copy_left = kb1 - kb0;
+  // The copy stream: the team's row groups, of each the warp's blocks of inputs.  An odd last
+  // tile is its own second.
+  int copy_rg = first_rg, copy_left = kb1 - kb0;
   uint32_t copy_dst = ring;
   const uint8_t *from = a.codes + copy_rg * RT * tile_codes + kb0 * 1024 + 16 * lane;
   const uint8_t *steps_from = reinterpret_cast<const uint8_t *>(a.scales) + copy_rg * RT * tile_steps +
                               (kb0 * 8 + (lane & 7)) * kScaleRow;
   int64_t second_codes = copy_rg * RT + 1 < s.tiles ? tile_codes : 0, second_steps = second_codes ? tile_steps : 0;
   griddep_launch_dependents();
-  if (lane < 8)
+  if (lane < 8 && first_rg < row_groups)
     for (int kb = kb0; kb < min(kb1, kb0 + kStages); ++kb) {
       const uint8_t *p = from + (kb - kb0) * 1024 + 112 * lane;  // 128 bytes a lane
       prefetch_l2(p);
@@ -306,9 +313,9 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
       steps_from += 8 * kScaleRow;
       if (--copy_left == 0) {
         copy_left = kb1 - kb0;
-        copy_rg += gridDim.x;
-        from += gridDim.x * (RT * tile_codes) - copy_left * 1024;
-        steps_from += gridDim.x * (RT * tile_steps) - copy_left * (8 * kScaleRow);
+        copy_rg += rg_step;
+        from += rg_step * (RT * tile_codes) - copy_left * 1024;
+        steps_from += rg_step * (RT * tile_steps) - copy_left * (8 * kScaleRow);
         if (copy_rg * RT + 1 >= s.tiles) second_codes = second_steps = 0;
       }
     }
@@ -332,10 +339,10 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
                       : make_uint4(0u, 0u, 0u, 0u);
   };
   uint4 x[NT][4];
-  if (kb0 < kb1) load_x(x, kb0);
+  if (NT == 1 && kb0 < kb1) load_x(x, kb0);
 
   int stage = 0, parity = 0;
-  for (int rg = blockIdx.x; rg < row_groups; rg += gridDim.x, parity ^= 1) {
+  for (int rg = first_rg; rg < row_groups; rg += rg_step, parity ^= 1) {
     float total[RT][NT][4];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -344,13 +351,15 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
 #pragma unroll
         for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
     for (int kb = kb0; kb < kb1; ++kb) {
+      if (NT == 2) load_x(x, kb);
       copy_wait<kStages - 2>();
       __syncwarp();
       fill();
       const uint32_t base = ring + stage * kStage;
-      // the next block's tokens; after the last block the first one's, for the next row group
+      // the next block's tokens where registers allow; after the last block the first one's,
+      // for the next row group
       uint4 ahead[NT][4];
-      load_x(ahead, kb + 1 < kb1 ? kb + 1 : kb0);
+      if (NT == 1) load_x(ahead, kb + 1 < kb1 ? kb + 1 : kb0);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         uint4 w0, w1;
@@ -393,12 +402,11 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
         }
       }
       stage = stage == kStages - 1 ? 0 : stage + 1;
+      if (NT == 1)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = ahead[n][j];
+        for (int j = 0; j < 4; ++j) x[0][j] = ahead[0][j];
     }
-    // the eighths meet; two sets of sums, so one barrier per row group is enough
+    // the team's parts meet; two sets of sums, so one barrier per row group is enough
 #pragma unroll
     for (int t = 0; t < RT; ++t)
 #pragma unroll
@@ -406,14 +414,17 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 2) group_gemv_kernel(GemvArgs
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           sums[parity][warp][8 * n + 2 * c + (e & 1)][16 * t + r + 8 * (e >> 1)] = total[t][n][e];
-    __syncthreads();
-    for (int i = tid; i < kRows * a.M; i += 32 * kGemvWarps) {
+    if (a.team == 1) {
+      __syncwarp();
+    } else {
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / a.team), "r"(32 * a.team) : "memory");
+    }
+    for (int i = 32 * part + lane; i < kRows * a.M; i += 32 * a.team) {
       const int row = i % kRows, m = i / kRows;
       const int64_t n = static_cast<int64_t>(rg) * kRows + row;
       if (n >= s.N) continue;
       float y = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kGemvWarps; ++w) y += sums[parity][w][m][row];
+      for (int w = warp - part; w < warp - part + a.team; ++w) y += sums[parity][w][m][row];
       if (a.bias) y += T::to_f32(a.bias[n]);
       uint16_t v = T::round(y);
       if (a.gelu) v = static_cast<uint16_t>(gelu_pair_bf16(v) & 0xFFFFu);
@@ -488,8 +499,9 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 }
 
 template <typename T, int GROUP, int RT, int NT>
-w4a4_status launch_gemv_t(const GemvArgs &a, void *stream) {
-  constexpr int kSmem = kGemvWarps * (RT == 1 ? 8 : 5) * RT * (1024 + 8 * 4 * (kBlockK / GROUP));
+w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
+  constexpr int kSmem = kGemvWarps * (gemv_stages(RT) * RT * (1024 + 8 * 4 * (kBlockK / GROUP)) +
+                                      2 * 4 * 8 * NT * (16 * RT + 1));
   static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
   int per_sm = 0;
   if (occupancy.get(&per_sm, [](int *v) {
@@ -501,9 +513,13 @@ w4a4_status launch_gemv_t(const GemvArgs &a, void *stream) {
         return e;
       }) != cudaSuccess || per_sm < 1)
     return W4A4_ERR_CUDA;
-  const int64_t need = (a.s.tiles + RT - 1) / RT, most = static_cast<int64_t>(device_sm_count()) * per_sm;
-  return launch_status(
-      launch(group_gemv_kernel<T, GROUP, RT, NT>, need < most ? need : most, 32 * kGemvWarps, kSmem, stream, a));
+  // Teams as small as keep the warps of every SM at work: a small team leaves more inputs
+  // to each warp and fewer sums to join.
+  const int64_t row_groups = (a.s.tiles + RT - 1) / RT, sms = device_sm_count();
+  a.team = 1;
+  while (a.team < kGemvWarps && a.team < a.s.blocks && 5 * row_groups * a.team < 4 * sms * kGemvWarps) a.team *= 2;
+  return launch_status(launch(group_gemv_kernel<T, GROUP, RT, NT>, row_groups < sms ? row_groups : sms,
+                              32 * kGemvWarps, kSmem, stream, a));
 }
 
 template <typename T, int GROUP>
@@ -585,7 +601,7 @@ w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weigh
   if (M == 0) return W4A4_OK;
   if (!X || !Y) return W4A4_ERR_ARG;
   if (!ptr_aligned16(X) || !ptr_aligned16(Y) || (bias && !ptr_aligned16(bias))) return W4A4_ERR_ALIGN;
-  const GemvArgs a{X, static_cast<int>(M), w->codes, w->scales, shape_of(w->N, w->K, w->group), bias, Y, gelu};
+  const GemvArgs a{X, static_cast<int>(M), w->codes, w->scales, shape_of(w->N, w->K, w->group), bias, Y, gelu, 0};
   switch (w->group) {
     case 32: return fp16 ? launch_gemv<Fp16, 32>(a, stream) : launch_gemv<Bf16, 32>(a, stream);
     case 64: return fp16 ? launch_gemv<Fp16, 64>(a, stream) : launch_gemv<Bf16, 64>(a, stream);
