@@ -220,15 +220,20 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    subtraction the exact codes.
 //  * A group's products are summed in fp32 by the tensor core, multiplied by the
 //    step and added to the fp32 total: the codes stay exact and no weight is rounded.
-//  * A block of 8 warps takes rows in tiles, its warps an eighth of the inputs each;
-//    a warp streams its codes and steps through its own ring of asynchronous copies,
-//    across the ends of tiles, and the eight sums meet in shared memory.
+//  * One block of 16 warps per SM takes an equal share of the 16-row tiles, up to RT at a
+//    time, and keeps their sums in registers.  The line (block of 128 inputs, tile)
+//    is cut evenly between the warps: a warp reads a block's tokens once and uses them for
+//    all the tiles, while codes and steps stream through its own ring of
+//    asynchronous copies.  At the end the warps' sums meet in shared memory, where the rings
+//    were.  (Tiles in pairs with the inputs split over the warps, so that every pair read
+//    all tokens again, took 34 us for 8 tokens at 32768 x 8192, half of it waiting for
+//    tokens that L1 could not hold.)
 //  * Before it waits for the kernel in front, a block asks for its first weights
 //    to be brought into L2: those do not depend on that kernel, and where they do
 //    (a quantization right before) L2 is where the new values appear.
 
 constexpr int kGemvWarps = 16;
-constexpr int gemv_stages(int RT) { return RT == 1 ? 6 : 3; }
+constexpr int kGemvStages = 8;
 
 struct GemvArgs {
   const uint16_t *X;
@@ -239,7 +244,7 @@ struct GemvArgs {
   const uint16_t *bias;
   uint16_t *Y;
   bool gelu;
-  int team;  // warps that share the inputs of a row group: 1, 2, 4, 8 or 16
+  int sets;  // sets of tiles, a multiple of the number of blocks; set i: tiles i * tiles / sets ..
 };
 
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -254,95 +259,101 @@ template <int BYTES>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void *src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// GROUP inputs per step, RT tiles of 16 rows per block, NT times 8 tokens.
+// GROUP inputs per step, at most RT tiles of 16 rows at a time, NT times 8 tokens.
 template <typename T, int GROUP, int RT, int NT>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs a) {
   constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
   constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
-  constexpr int kStage = RT * (1024 + 8 * kScaleRow);
-  constexpr int kStages = gemv_stages(RT);
-  constexpr int kRows = 16 * RT, kCols = 8 * NT;
+  constexpr int kStage = 1024 + 8 * kScaleRow;
+  constexpr int kCols = 8 * NT, kTileSums = 16 * kCols;
+  constexpr bool kAhead = RT * NT <= 4;             // registers for the next block's tokens
   extern __shared__ __align__(128) uint8_t smem[];
-  typedef float Sums[kGemvWarps][kCols][kRows + 1];
-  Sums *sums = reinterpret_cast<Sums *>(smem + kGemvWarps * kStages * kStage);  // [2]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const GroupShape &s = a.s;
-  // this warp's part of the inputs, and its team's first row group and stride: teams of one
-  // number over all blocks come first, so that SMs get equally many
-  const int part = warp % a.team, first_rg = blockIdx.x + gridDim.x * (warp / a.team);
-  const int rg_step = gridDim.x * (kGemvWarps / a.team);
-  const int kb0 = static_cast<int>(static_cast<int64_t>(part) * s.blocks / a.team);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(part + 1) * s.blocks / a.team);
-  const int row_groups = (s.tiles + RT - 1) / RT;
-  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  const uint32_t ring = smem_u32(smem) + warp * kGemvStages * kStage;
   const int64_t tile_codes = static_cast<int64_t>(s.blocks) * 1024;
   const int64_t tile_steps = static_cast<int64_t>(s.blocks) * 8 * kScaleRow;
-
-  // The copy stream: the team's row groups, of each the warp's blocks of inputs.  An odd last
-  // tile is its own second.
-  int copy_rg = first_rg, copy_left = kb1 - kb0;
-  uint32_t copy_dst = ring;
-  const uint8_t *from = a.codes + copy_rg * RT * tile_codes + kb0 * 1024 + 16 * lane;
-  const uint8_t *steps_from = reinterpret_cast<const uint8_t *>(a.scales) + copy_rg * RT * tile_steps +
-                              (kb0 * 8 + (lane & 7)) * kScaleRow;
-  int64_t second_codes = copy_rg * RT + 1 < s.tiles ? tile_codes : 0, second_steps = second_codes ? tile_steps : 0;
-  griddep_launch_dependents();
-  if (lane < 8 && first_rg < row_groups)
-    for (int kb = kb0; kb < min(kb1, kb0 + kStages); ++kb) {
-      const uint8_t *p = from + (kb - kb0) * 1024 + 112 * lane;  // 128 bytes a lane
-      prefetch_l2(p);
-      if (RT == 2) prefetch_l2(p + second_codes);
-    }
-  griddep_wait();
-  auto fill = [&]() {
-    if (copy_rg < row_groups && kb0 < kb1) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const uint8_t *f = t ? from + second_codes : from;
-        copy16(copy_dst + t * 1024 + 16 * lane, f);
-        copy16(copy_dst + t * 1024 + 512 + 16 * lane, f + 512);
-        if (lane < 8)
-          copy_small<kScaleRow>(copy_dst + RT * 1024 + (t * 8 + lane) * kScaleRow,
-                                t ? steps_from + second_steps : steps_from);
-      }
-      copy_dst = copy_dst == ring + (kStages - 1) * kStage ? ring : copy_dst + kStage;
-      from += 1024;
-      steps_from += 8 * kScaleRow;
-      if (--copy_left == 0) {
-        copy_left = kb1 - kb0;
-        copy_rg += rg_step;
-        from += rg_step * (RT * tile_codes) - copy_left * 1024;
-        steps_from += rg_step * (RT * tile_steps) - copy_left * (8 * kScaleRow);
-        if (copy_rg * RT + 1 >= s.tiles) second_codes = second_steps = 0;
-      }
-    }
-    copy_commit();
-  };
-#pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) fill();
-
   // Tokens r and r + 8 as the B operand; columns behind the last token repeat it
   // (their sums are not used).
   const uint16_t *x_row[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) x_row[n] = a.X + static_cast<int64_t>(min(8 * n + r, a.M - 1)) * s.K + 8 * c;
   auto load_x = [&](uint4 (&x)[NT][4], int kb) {
+    const int k = kb * kBlockK;
+    if (k + kBlockK <= s.K) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        x[n][j] = kb * kBlockK + 32 * j < s.K
-                      ? __ldg(reinterpret_cast<const uint4 *>(x_row[n] + kb * kBlockK + 32 * j))
-                      : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < 4; ++j) x[n][j] = __ldg(reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j));
+    } else {  // the padding's codes are 0, but what stands behind a token may not be finite
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          x[n][j] = k + 32 * j < s.K ? __ldg(reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+    }
   };
-  uint4 x[NT][4];
-  if (NT == 1 && kb0 < kb1) load_x(x, kb0);
 
-  int stage = 0, parity = 0;
-  for (int rg = first_rg; rg < row_groups; rg += rg_step, parity ^= 1) {
+  griddep_launch_dependents();
+  for (int set = blockIdx.x; set < a.sets; set += gridDim.x) {
+    const int tile0 = static_cast<int>(static_cast<int64_t>(set) * s.tiles / a.sets);
+    const int tiles = static_cast<int>(static_cast<int64_t>(set + 1) * s.tiles / a.sets) - tile0;
+    // this warp's part of the line
+    const int begin = static_cast<int>(static_cast<int64_t>(warp) * s.blocks * tiles / kGemvWarps);
+    const int end = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks * tiles / kGemvWarps);
+    int kb = begin / tiles, t0 = begin - kb * tiles, left = end - begin;
+    // the copies' place in it
+    int copy_t = t0, copy_left = left;
+    uint32_t copy_dst = ring;
+    const uint8_t *from = a.codes + (tile0 + t0) * tile_codes + static_cast<int64_t>(kb) * 1024 + 16 * lane;
+    const uint8_t *steps_from = reinterpret_cast<const uint8_t *>(a.scales) + (tile0 + t0) * tile_steps +
+                                (static_cast<int64_t>(kb) * 8 + (lane & 7)) * kScaleRow;
+    auto advance = [&]() {
+      from += tile_codes;
+      steps_from += tile_steps;
+      if (++copy_t == tiles) {
+        copy_t = 0;
+        from += 1024 - tiles * tile_codes;
+        steps_from += 8 * kScaleRow - tiles * tile_steps;
+      }
+    };
+    if (set == blockIdx.x) {
+      const uint8_t *const from0 = from, *const steps0 = steps_from;
+      for (int i = 0; i < min(left, kGemvStages - 1); ++i) {
+        if (lane < 8) prefetch_l2(from + 112 * lane);  // 128 bytes a lane
+        advance();
+      }
+      from = from0, steps_from = steps0, copy_t = t0;
+      griddep_wait();
+    }
+    auto fill = [&]() {
+      if (copy_left > 0) {
+        copy16(copy_dst + 16 * lane, from);
+        copy16(copy_dst + 512 + 16 * lane, from + 512);
+        if (lane < 8) copy_small<kScaleRow>(copy_dst + 1024 + lane * kScaleRow, steps_from);
+        copy_dst = copy_dst == ring + (kGemvStages - 1) * kStage ? ring : copy_dst + kStage;
+        --copy_left;
+        advance();
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int i = 0; i < kGemvStages - 1; ++i) fill();
+
     float total[RT][NT][4];
 #pragma unroll
     for (int t = 0; t < RT; ++t)
@@ -350,46 +361,44 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
-    for (int kb = kb0; kb < kb1; ++kb) {
-      if (NT == 2) load_x(x, kb);
-      copy_wait<kStages - 2>();
-      __syncwarp();
-      fill();
-      const uint32_t base = ring + stage * kStage;
-      // the next block's tokens where registers allow; after the last block the first one's,
-      // for the next row group
-      uint4 ahead[NT][4];
-      if (NT == 1) load_x(ahead, kb + 1 < kb1 ? kb + 1 : kb0);
+    uint4 x[NT][4], ahead[NT][4];
+    if (kAhead && left > 0) load_x(ahead, kb);
+    uint32_t stage = ring;
+    while (left > 0) {
+      const int t1 = min(tiles, t0 + left);  // tiles t0 .. t1 - 1 of block kb
+      if (kAhead) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[n][j] = ahead[n][j];
+        if (left > t1 - t0) load_x(ahead, kb + 1);
+      } else {
+        load_x(x, kb);
+      }
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        uint4 w0, w1;
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w0.x), "=r"(w0.y), "=r"(w0.z), "=r"(w0.w) : "r"(base + t * 1024 + 16 * lane));
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w1.x), "=r"(w1.y), "=r"(w1.z), "=r"(w1.w) : "r"(base + t * 1024 + 512 + 16 * lane));
+        if (t < t0 || t >= t1) continue;
+        copy_wait<kGemvStages - 2>();
+        __syncwarp();
+        fill();
+        const uint4 w0 = lds16(stage + 16 * lane), w1 = lds16(stage + 512 + 16 * lane);
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
         float part[NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (j % (GROUP / 32) == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) part[n][e] = 0.0f;
-          }
           uint32_t p[4], q[4];
           T::codes(lo[j], p);
           T::codes(hi[j], q);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            T::mma(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
+            if (j % (GROUP / 32) == 0)
+              T::mma0(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
+            else
+              T::mma(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
             T::mma(part[n], p[2], q[2], p[3], q[3], x[n][j].z, x[n][j].w);
           }
           if ((j + 1) % (GROUP / 32) == 0) {
-            uint32_t steps;
-            asm volatile("ld.shared.u32 %0, [%1];"
-                         : "=r"(steps)
-                         : "r"(base + RT * 1024 + (t * 8 + r) * kScaleRow + 4 * (j / (GROUP / 32))));
+            const uint32_t steps = lds4(stage + 1024 + r * kScaleRow + 4 * (j / (GROUP / 32)));
             const float s0 = T::lo(steps), s1 = T::hi(steps);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -400,38 +409,38 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
             }
           }
         }
+        stage = stage == ring + (kGemvStages - 1) * kStage ? ring : stage + kStage;
       }
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      if (NT == 1)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[0][j] = ahead[0][j];
+      left -= t1 - t0;
+      t0 = 0;
+      ++kb;
     }
-    // the team's parts meet; two sets of sums, so one barrier per row group is enough
+    copy_wait<0>();
+    __syncthreads();  // the rings are free: [warp][tile][row][token]
+    float *sums = reinterpret_cast<float *>(smem);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
+      if (t < tiles)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          sums[parity][warp][8 * n + 2 * c + (e & 1)][16 * t + r + 8 * (e >> 1)] = total[t][n][e];
-    if (a.team == 1) {
-      __syncwarp();
-    } else {
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / a.team), "r"(32 * a.team) : "memory");
-    }
-    for (int i = 32 * part + lane; i < kRows * a.M; i += 32 * a.team) {
-      const int row = i % kRows, m = i / kRows;
-      const int64_t n = static_cast<int64_t>(rg) * kRows + row;
-      if (n >= s.N) continue;
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<float2 *>(&sums[(warp * tiles + t) * kTileSums + (r + 8 * h) * kCols + 8 * n + 2 * c]) =
+                make_float2(total[t][n][2 * h], total[t][n][2 * h + 1]);
+    __syncthreads();
+    for (int i = tid; i < tiles * kTileSums; i += 32 * kGemvWarps) {
+      const int m = i % kCols, n = tile0 * kTileRows + i / kCols;
+      if (m >= a.M || n >= s.N) continue;
       float y = 0.0f;
-      for (int w = warp - part; w < warp - part + a.team; ++w) y += sums[parity][w][m][row];
+#pragma unroll
+      for (int w = 0; w < kGemvWarps; ++w) y += sums[w * tiles * kTileSums + i];
       if (a.bias) y += T::to_f32(a.bias[n]);
       uint16_t v = T::round(y);
       if (a.gelu) v = static_cast<uint16_t>(gelu_pair_bf16(v) & 0xFFFFu);
       a.Y[m * static_cast<int64_t>(s.N) + n] = v;
     }
+    __syncthreads();  // before the rings are filled again
   }
-  copy_wait<0>();
 }
 
 constexpr uint32_t kGroupFlags = W4A4_FLAG_FP16;
@@ -500,34 +509,31 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kSmem = kGemvWarps * (gemv_stages(RT) * RT * (1024 + 8 * 4 * (kBlockK / GROUP)) +
-                                      2 * 4 * 8 * NT * (16 * RT + 1));
-  static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
-  int per_sm = 0;
-  if (occupancy.get(&per_sm, [](int *v) {
-        cudaError_t e = cudaFuncSetAttribute(group_gemv_kernel<T, GROUP, RT, NT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-        if (e == cudaSuccess)
-          e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, group_gemv_kernel<T, GROUP, RT, NT>, 32 * kGemvWarps,
-                                                            kSmem);
-        return e;
-      }) != cudaSuccess || per_sm < 1)
+  constexpr int kRing = kGemvWarps * kGemvStages * (1024 + 8 * 4 * (kBlockK / GROUP));
+  constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
+  static ContextCache<int> ready;  // per context: attribute set
+  int done = 0;
+  if (ready.get(&done, [](int *v) {
+        *v = 1;
+        return cudaFuncSetAttribute(group_gemv_kernel<T, GROUP, RT, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmem);
+      }) != cudaSuccess)
     return W4A4_ERR_CUDA;
-  // Teams as small as keep the warps of every SM at work: a small team leaves more inputs
-  // to each warp and fewer sums to join.
-  const int64_t row_groups = (a.s.tiles + RT - 1) / RT, sms = device_sm_count();
-  a.team = 1;
-  while (a.team < kGemvWarps && a.team < a.s.blocks && 5 * row_groups * a.team < 4 * sms * kGemvWarps) a.team *= 2;
-  return launch_status(launch(group_gemv_kernel<T, GROUP, RT, NT>, row_groups < sms ? row_groups : sms,
-                              32 * kGemvWarps, kSmem, stream, a));
+  const int sms = device_sm_count(), grid = a.s.tiles < sms ? a.s.tiles : sms;
+  a.sets = ((a.s.tiles - 1) / (grid * RT) + 1) * grid;
+  return launch_status(launch(group_gemv_kernel<T, GROUP, RT, NT>, grid, 32 * kGemvWarps, kSmem, stream, a));
 }
 
 template <typename T, int GROUP>
 w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
-  // two tiles per block share every token operand; one where that would leave SMs idle
-  const bool two = a.s.tiles >= 4 * device_sm_count();
-  if (a.M <= 8) return two ? launch_gemv_t<T, GROUP, 2, 1>(a, stream) : launch_gemv_t<T, GROUP, 1, 1>(a, stream);
-  return two ? launch_gemv_t<T, GROUP, 2, 2>(a, stream) : launch_gemv_t<T, GROUP, 1, 2>(a, stream);
+  // as many tiles at a time as a block has, up to what its registers hold
+  const int tiles = (a.s.tiles - 1) / device_sm_count() + 1;
+  if (a.M <= 8) {
+    if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 1>(a, stream);
+    return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 1>(a, stream) : launch_gemv_t<T, GROUP, 16, 1>(a, stream);
+  }
+  if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 2>(a, stream);
+  return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 2>(a, stream) : launch_gemv_t<T, GROUP, 8, 2>(a, stream);
 }
 
 }  // namespace
