@@ -47,27 +47,27 @@ extern "C" {
 /* ------------------------------------------- 4-bit weights with group steps */
 
 /* Weights W [N, K] as codes c in [-8, 7] and steps s, one per group of `group`
- * consecutive inputs of a row: W[n, k] ~ c[n, k] * s[n, k / group].  Both arrays
- * are in the order the kernels read (w4a4_group_pack and w4a4_group_quantize
- * write it): rows in tiles of 16 and inputs in blocks of 128, both padded with
- * zeros.  Within a tile and block, the codes of rows r and r + 8 (r = 0..7) form
- * two runs of 512 bytes; 16 bytes at 64 r + 16 c of a run (c = 0..3) hold four
- * words, word j the 8 codes of inputs 32 j + 8 c + 0..7 of the block, inputs
- * 0, 2, 4, 6, 1, 3, 5, 7 from the lowest nibble up. */
+ * consecutive inputs of a row: W[n, k] ~ c[n, k] * s[n, k / group], in the order
+ * the kernels read (w4a4_group_pack and w4a4_group_quantize write it): rows in
+ * tiles of 16 and inputs in blocks of 128, both padded with zeros, one record of
+ * 1024 + 4096 / group bytes after another, the blocks of a tile in a row.  In a record, the
+ * codes of rows r and r + 8 (r = 0..7) form two runs of 512 bytes; 16 bytes at 64 r
+ * + 16 c of a run (c = 0..3) hold four words, word j the 8 codes of inputs 32 j +
+ * 8 c + 0..7 of the block, inputs 0, 2, 4, 6, 1, 3, 5, 7 from the lowest nibble up.
+ * Then follow, for r = 0..7, the 16-bit steps of rows r and r + 8 for each group. */
 typedef struct {
     int32_t N;         /* rows, 1 .. 16777216 */
     int32_t K;         /* inputs, a positive multiple of group, <= 1048576 */
     int32_t group;     /* 32, 64 or 128 */
     uint32_t flags;    /* 0 or W4A4_FLAG_FP16: type of steps, weights and tokens */
-    uint8_t *codes;
-    uint16_t *scales;
+    uint8_t *data;
 } w4a4_group_weights_t;
 
-/* Bytes of one device allocation that holds both arrays; 0 for an N, K or group
- * that is not accepted.  About N K / 2 + 2 N K / group. */
+/* Bytes of the records; 0 for an N, K or group that is not accepted.  About
+ * N K / 2 + 2 N K / group. */
 size_t w4a4_group_weights_bytes(int32_t N, int32_t K, int32_t group);
 
-/* Points *out into `base` (16-byte aligned, at least
+/* Points *out at `base` (16-byte aligned, at least
  * w4a4_group_weights_bytes(N, K, group) bytes, owned by the caller) and fills in
  * the sizes.  flags: 0 or W4A4_FLAG_FP16.  Touches no device memory.
  * W4A4_ERR_UNSUPPORTED for another group or flag, W4A4_ERR_SHAPE for an N, K or

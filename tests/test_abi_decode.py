@@ -18,7 +18,7 @@ FP16, PAIRS, GELU_OUT = 0x200, 0x400, 0x10
 
 
 class GroupT(ctypes.Structure):
-    _fields_ = [("N", i32), ("K", i32), ("group", i32), ("flags", u32), ("codes", vp), ("scales", vp)]
+    _fields_ = [("N", i32), ("K", i32), ("group", i32), ("flags", u32), ("data", vp)]
 
 
 class CacheT(ctypes.Structure):
@@ -49,20 +49,19 @@ def lib():
     return L
 
 
-def _group(N=256, K=512, group=64, flags=0, codes=A, scales=A):
-    return ctypes.byref(GroupT(N, K, group, flags, codes, scales))
+def _group(N=256, K=512, group=64, flags=0, data=A):
+    return ctypes.byref(GroupT(N, K, group, flags, data))
 
 
 def test_group_weights_layout(lib):
     bytes_ = lib.w4a4_group_weights_bytes
     for N, K, g in [(256, 512, 64), (1, 32, 32), (17, 160, 32), (1021, 4096, 128), (16, 128, 64)]:
-        tiles, blocks = -(-N // 16), -(-K // 128)
-        codes, scales = tiles * blocks * 1024, tiles * blocks * 16 * (128 // g) * 2
-        assert bytes_(N, K, g) == (codes + 255) // 256 * 256 + scales
+        # per 16 rows and 128 inputs 1024 bytes of codes and 16 rows' steps
+        assert bytes_(N, K, g) == -(-N // 16) * -(-K // 128) * (1024 + 16 * (128 // g) * 2)
         out = GroupT()
         assert lib.w4a4_group_bind(A, bytes_(N, K, g), N, K, g, FP16, ctypes.byref(out)) == OK
         assert (out.N, out.K, out.group, out.flags) == (N, K, g, FP16)
-        assert out.codes == A and out.scales == A + (codes + 255) // 256 * 256
+        assert out.data == A
         assert lib.w4a4_group_bind(A, bytes_(N, K, g) - 1, N, K, g, 0, ctypes.byref(out)) == SHAPE
     for N, K, g in [(0, 512, 64), (-1, 512, 64), (256, 0, 64), (256, 96, 64), (256, 512, 16), (256, 512, 256),
                     (256, (1 << 20) + 128, 128), (0x7FFFFFFF, 128, 128),
@@ -80,8 +79,7 @@ def test_group_weights_layout(lib):
 def test_group_argument_checks(lib):
     Q, P, D, G = lib.w4a4_group_quantize, lib.w4a4_group_pack, lib.w4a4_group_dequantize, lib.w4a4_group_gemv
     bad = [(None, ARG), (_group(group=16), UNSUPPORTED), (_group(flags=0x2), UNSUPPORTED), (_group(N=0), SHAPE),
-           (_group(K=500), SHAPE), (_group(codes=None), ARG), (_group(scales=None), ARG),
-           (_group(codes=A + 4), ALIGN), (_group(scales=A + 2), ALIGN)]
+           (_group(K=500), SHAPE), (_group(data=None), ARG), (_group(data=A + 4), ALIGN)]
     for w, want in bad:
         assert Q(A, w, None) == want
         assert P(A, A, w, None) == want

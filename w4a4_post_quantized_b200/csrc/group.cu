@@ -22,6 +22,10 @@ struct GroupShape {
   int tiles, blocks;  // ceil(N / 16), ceil(K / 128)
 };
 
+// Bytes of the record of a tile and block: 1024 of codes, then for r = 0..7 the
+// steps of rows r and r + 8, group by group.
+__host__ __device__ constexpr int record_bytes(int group) { return 1024 + 32 * (kBlockK / group); }
+
 // Nibble of element e (0..7) in a word: 0, 2, 4, 6, 1, 3, 5, 7 from the lowest up.
 __device__ __forceinline__ int nibble_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
 
@@ -73,8 +77,7 @@ __device__ __noinline__ int slow_code(float x, float step) {
 
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_quantize_kernel(const uint16_t *__restrict__ W, GroupShape s, uint8_t *__restrict__ codes,
-                          uint16_t *__restrict__ scales) {
+    group_quantize_kernel(const uint16_t *__restrict__ W, GroupShape s, uint8_t *__restrict__ data) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;  // groups of a block, words j of a group
   griddep_launch_dependents();
   griddep_wait();
@@ -130,24 +133,25 @@ __global__ void __launch_bounds__(32 * kPackWarps)
         word[j] = w;
       }
     }
-    *reinterpret_cast<uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane) =
+    *reinterpret_cast<uint4 *>(data + u.at * record_bytes(GROUP) + 512 * h + 16 * lane) =
         make_uint4(word[0], word[1], word[2], word[3]);
   }
   if ((lane & 3) == 0) {
-    uint32_t *to = reinterpret_cast<uint32_t *>(scales) + (u.at * 8 + (lane >> 2)) * kPer;
+    uint32_t *to = reinterpret_cast<uint32_t *>(data + u.at * record_bytes(GROUP) + 1024) + (lane >> 2) * kPer;
 #pragma unroll
     for (int g = 0; g < kPer; ++g) to[g] = steps[g];
   }
 }
 
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_pack_kernel(const uint8_t *__restrict__ plain, const uint16_t *__restrict__ steps, GroupShape s,
-                      uint8_t *__restrict__ codes, uint16_t *__restrict__ scales) {
+    group_pack_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, GroupShape s,
+                      uint8_t *__restrict__ data) {
   griddep_launch_dependents();
   griddep_wait();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31, per = kBlockK / s.group;
+  uint8_t *record = data + u.at * record_bytes(s.group);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = u.row + 8 * h;
@@ -156,39 +160,38 @@ __global__ void __launch_bounds__(32 * kPackWarps)
     for (int j = 0; j < 4; ++j) {
       uint32_t v = 0, w = 0;
       if (n < s.N && u.k + 32 * j < s.K)
-        v = *reinterpret_cast<const uint32_t *>(plain + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
+        v = *reinterpret_cast<const uint32_t *>(codes + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << nibble_shift(e);
       word[j] = w;
     }
-    *reinterpret_cast<uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane) =
+    *reinterpret_cast<uint4 *>(record + 512 * h + 16 * lane) =
         make_uint4(word[0], word[1], word[2], word[3]);
     const int g0 = (u.k / kBlockK) * per, groups = s.K / s.group;
     if ((lane & 3) < per) {
       const int g = lane & 3;
-      scales[((u.at * 8 + (lane >> 2)) * per + g) * 2 + h] =
-          n < s.N && g0 + g < groups ? steps[static_cast<int64_t>(n) * groups + g0 + g] : uint16_t(0);
+      reinterpret_cast<uint16_t *>(record + 1024)[((lane >> 2) * per + g) * 2 + h] =
+          n < s.N && g0 + g < groups ? scales[static_cast<int64_t>(n) * groups + g0 + g] : uint16_t(0);
     }
   }
 }
 
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_dequantize_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, GroupShape s,
-                            uint16_t *__restrict__ W) {
+    group_dequantize_kernel(const uint8_t *__restrict__ data, GroupShape s, uint16_t *__restrict__ W) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;
   griddep_launch_dependents();
   griddep_wait();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31;
+  const uint8_t *record = data + u.at * record_bytes(GROUP);
   uint32_t steps[kPer];
 #pragma unroll
-  for (int g = 0; g < kPer; ++g)
-    steps[g] = reinterpret_cast<const uint32_t *>(scales)[(u.at * 8 + (lane >> 2)) * kPer + g];
+  for (int g = 0; g < kPer; ++g) steps[g] = reinterpret_cast<const uint32_t *>(record + 1024)[(lane >> 2) * kPer + g];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(codes + u.at * 1024 + 512 * h + 16 * lane));
+    const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(record + 512 * h + 16 * lane));
     const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -238,8 +241,7 @@ constexpr int kGemvStages = 8;
 struct GemvArgs {
   const uint16_t *X;
   int M;
-  const uint8_t *codes;
-  const uint16_t *scales;
+  const uint8_t *data;
   GroupShape s;
   const uint16_t *bias;
   uint16_t *Y;
@@ -254,10 +256,6 @@ __device__ __forceinline__ void copy_wait() {
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-template <int BYTES>
-__device__ __forceinline__ void copy_small(uint32_t dst, const void *src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
   uint4 v;
@@ -276,7 +274,7 @@ template <typename T, int GROUP, int RT, int NT>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs a) {
   constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
   constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
-  constexpr int kStage = 1024 + 8 * kScaleRow;
+  constexpr int kStage = record_bytes(GROUP);
   constexpr int kCols = 8 * NT, kTileSums = 16 * kCols;
   constexpr bool kAhead = RT * NT <= 4;             // registers for the next block's tokens
   extern __shared__ __align__(128) uint8_t smem[];
@@ -284,8 +282,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
   const int r = lane >> 2, c = lane & 3;
   const GroupShape &s = a.s;
   const uint32_t ring = smem_u32(smem) + warp * kGemvStages * kStage;
-  const int64_t tile_codes = static_cast<int64_t>(s.blocks) * 1024;
-  const int64_t tile_steps = static_cast<int64_t>(s.blocks) * 8 * kScaleRow;
+  const int64_t tile_bytes = static_cast<int64_t>(s.blocks) * kStage;
   // Tokens r and r + 8 as the B operand; columns behind the last token repeat it
   // (their sums are not used).
   const uint16_t *x_row[NT];
@@ -316,37 +313,31 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
     const int begin = static_cast<int>(static_cast<int64_t>(warp) * s.blocks * tiles / kGemvWarps);
     const int end = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks * tiles / kGemvWarps);
     int kb = begin / tiles, t0 = begin - kb * tiles, left = end - begin;
-    // the copies' place in it
-    int copy_t = t0, copy_left = left;
-    uint32_t copy_dst = ring;
-    const uint8_t *from = a.codes + (tile0 + t0) * tile_codes + static_cast<int64_t>(kb) * 1024 + 16 * lane;
-    const uint8_t *steps_from = reinterpret_cast<const uint8_t *>(a.scales) + (tile0 + t0) * tile_steps +
-                                (static_cast<int64_t>(kb) * 8 + (lane & 7)) * kScaleRow;
+    // the copies' place in it: records until the next block of inputs, and in all
+    const int64_t to_next = kStage - (tiles - 1) * tile_bytes;  // from the last tile to the next block's first
+    int copy_t = tiles - t0, copies = left;
+    uint32_t copy_dst = ring + 16 * lane;
+    const uint32_t last = ring + (kGemvStages - 1) * kStage;
+    const uint8_t *from = a.data + (tile0 + t0) * tile_bytes + static_cast<int64_t>(kb) * kStage + 16 * lane;
     auto advance = [&]() {
-      from += tile_codes;
-      steps_from += tile_steps;
-      if (++copy_t == tiles) {
-        copy_t = 0;
-        from += 1024 - tiles * tile_codes;
-        steps_from += 8 * kScaleRow - tiles * tile_steps;
-      }
+      from += --copy_t ? tile_bytes : to_next;
+      if (copy_t == 0) copy_t = tiles;
     };
     if (set == blockIdx.x) {
-      const uint8_t *const from0 = from, *const steps0 = steps_from;
+      const uint8_t *const from0 = from;
       for (int i = 0; i < min(left, kGemvStages - 1); ++i) {
-        if (lane < 8) prefetch_l2(from + 112 * lane);  // 128 bytes a lane
+        if (128 * lane < kStage) prefetch_l2(from + 112 * lane);  // 128 bytes a lane
         advance();
       }
-      from = from0, steps_from = steps0, copy_t = t0;
+      from = from0, copy_t = tiles - t0;
       griddep_wait();
     }
     auto fill = [&]() {
-      if (copy_left > 0) {
-        copy16(copy_dst + 16 * lane, from);
-        copy16(copy_dst + 512 + 16 * lane, from + 512);
-        if (lane < 8) copy_small<kScaleRow>(copy_dst + 1024 + lane * kScaleRow, steps_from);
-        copy_dst = copy_dst == ring + (kGemvStages - 1) * kStage ? ring : copy_dst + kStage;
-        --copy_left;
+      if (--copies >= 0) {
+        copy16(copy_dst, from);
+        copy16(copy_dst + 512, from + 512);
+        if (lane < 2 * kPer) copy16(copy_dst + 1024, from + 1024);
+        copy_dst = copy_dst >= last ? ring + 16 * lane : copy_dst + kStage;
         advance();
       }
       copy_commit();
@@ -363,7 +354,8 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
         for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
     uint4 x[NT][4], ahead[NT][4];
     if (kAhead && left > 0) load_x(ahead, kb);
-    uint32_t stage = ring;
+    uint32_t stage = ring + 16 * lane;
+    const int steps_at = 1024 + r * kScaleRow - 16 * lane;
     while (left > 0) {
       const int t1 = min(tiles, t0 + left);  // tiles t0 .. t1 - 1 of block kb
       if (kAhead) {
@@ -381,7 +373,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
         copy_wait<kGemvStages - 2>();
         __syncwarp();
         fill();
-        const uint4 w0 = lds16(stage + 16 * lane), w1 = lds16(stage + 512 + 16 * lane);
+        const uint4 w0 = lds16(stage), w1 = lds16(stage + 512);
         const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
         float part[NT][4];
 #pragma unroll
@@ -398,7 +390,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
             T::mma(part[n], p[2], q[2], p[3], q[3], x[n][j].z, x[n][j].w);
           }
           if ((j + 1) % (GROUP / 32) == 0) {
-            const uint32_t steps = lds4(stage + 1024 + r * kScaleRow + 4 * (j / (GROUP / 32)));
+            const uint32_t steps = lds4(stage + steps_at + 4 * (j / (GROUP / 32)));
             const float s0 = T::lo(steps), s1 = T::hi(steps);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -409,7 +401,7 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
             }
           }
         }
-        stage = stage == ring + (kGemvStages - 1) * kStage ? ring : stage + kStage;
+        stage = stage >= last ? ring + 16 * lane : stage + kStage;
       }
       left -= t1 - t0;
       t0 = 0;
@@ -454,18 +446,12 @@ GroupShape shape_of(int32_t N, int32_t K, int32_t group) {
   return {N, K, group, (N - 1) / kTileRows + 1, (K + kBlockK - 1) / kBlockK};
 }
 
-size_t code_bytes(const GroupShape &s) { return static_cast<size_t>(s.tiles) * s.blocks * 1024; }
-size_t scale_bytes(const GroupShape &s) {
-  return static_cast<size_t>(s.tiles) * s.blocks * (16 * (kBlockK / s.group)) * 2;
-}
-size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
-
 w4a4_status check_group(const w4a4_group_weights_t *w) {
   if (!w) return W4A4_ERR_ARG;
   if (!group_ok(w->group) || (w->flags & ~kGroupFlags)) return W4A4_ERR_UNSUPPORTED;
   if (!group_shape_ok(w->N, w->K, w->group)) return W4A4_ERR_SHAPE;
-  if (!w->codes || !w->scales) return W4A4_ERR_ARG;
-  if (!ptr_aligned16(w->codes) || !ptr_aligned16(w->scales)) return W4A4_ERR_ALIGN;
+  if (!w->data) return W4A4_ERR_ARG;
+  if (!ptr_aligned16(w->data)) return W4A4_ERR_ALIGN;
   return W4A4_OK;
 }
 
@@ -495,7 +481,7 @@ w4a4_status launch_quantize(const uint16_t *W, const w4a4_group_weights_t *w, vo
   auto kern = w->group == 32   ? group_quantize_kernel<T, 32>
               : w->group == 64 ? group_quantize_kernel<T, 64>
                                : group_quantize_kernel<T, 128>;
-  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, W, s, w->codes, w->scales));
+  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, W, s, w->data));
 }
 
 template <typename T>
@@ -504,12 +490,12 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
   auto kern = w->group == 32   ? group_dequantize_kernel<T, 32>
               : w->group == 64 ? group_dequantize_kernel<T, 64>
                                : group_dequantize_kernel<T, 128>;
-  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, w->codes, w->scales, s, W));
+  return launch_status(launch(kern, pack_grid(s), 32 * kPackWarps, 0, stream, w->data, s, W));
 }
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kRing = kGemvWarps * kGemvStages * (1024 + 8 * 4 * (kBlockK / GROUP));
+  constexpr int kRing = kGemvWarps * kGemvStages * record_bytes(GROUP);
   constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
   static ContextCache<int> ready;  // per context: attribute set
   int done = 0;
@@ -545,7 +531,7 @@ size_t w4a4_group_weights_bytes(int32_t N, int32_t K, int32_t group) {
   using namespace w4a4;
   if (!group_ok(group) || !group_shape_ok(N, K, group)) return 0;
   const GroupShape s = shape_of(N, K, group);
-  return round256(code_bytes(s)) + scale_bytes(s);
+  return static_cast<size_t>(s.tiles) * s.blocks * record_bytes(group);
 }
 
 w4a4_status w4a4_group_bind(void *base, size_t bytes, int32_t N, int32_t K, int32_t group, uint32_t flags,
@@ -556,13 +542,11 @@ w4a4_status w4a4_group_bind(void *base, size_t bytes, int32_t N, int32_t K, int3
   if (!ptr_aligned16(base)) return W4A4_ERR_ALIGN;
   if (!group_shape_ok(N, K, group)) return W4A4_ERR_SHAPE;
   if (bytes < w4a4_group_weights_bytes(N, K, group)) return W4A4_ERR_SHAPE;
-  uint8_t *b = static_cast<uint8_t *>(base);
   out->N = N;
   out->K = K;
   out->group = group;
   out->flags = flags;
-  out->codes = b;
-  out->scales = reinterpret_cast<uint16_t *>(b + round256(code_bytes(shape_of(N, K, group))));
+  out->data = static_cast<uint8_t *>(base);
   return W4A4_OK;
 }
 
@@ -584,7 +568,7 @@ w4a4_status w4a4_group_pack(const uint8_t *codes, const uint16_t *scales, const 
   if (!ptr_aligned16(codes) || !ptr_aligned16(scales)) return W4A4_ERR_ALIGN;
   const GroupShape s = shape_of(w->N, w->K, w->group);
   return launch_status(
-      launch(group_pack_kernel, pack_grid(s), 32 * kPackWarps, 0, stream, codes, scales, s, w->codes, w->scales));
+      launch(group_pack_kernel, pack_grid(s), 32 * kPackWarps, 0, stream, codes, scales, s, w->data));
 }
 
 w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *stream) {
@@ -607,7 +591,7 @@ w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weigh
   if (M == 0) return W4A4_OK;
   if (!X || !Y) return W4A4_ERR_ARG;
   if (!ptr_aligned16(X) || !ptr_aligned16(Y) || (bias && !ptr_aligned16(bias))) return W4A4_ERR_ALIGN;
-  const GemvArgs a{X, static_cast<int>(M), w->codes, w->scales, shape_of(w->N, w->K, w->group), bias, Y, gelu, 0};
+  const GemvArgs a{X, static_cast<int>(M), w->data, shape_of(w->N, w->K, w->group), bias, Y, gelu, 0};
   switch (w->group) {
     case 32: return fp16 ? launch_gemv<Fp16, 32>(a, stream) : launch_gemv<Bf16, 32>(a, stream);
     case 64: return fp16 ? launch_gemv<Fp16, 64>(a, stream) : launch_gemv<Bf16, 64>(a, stream);

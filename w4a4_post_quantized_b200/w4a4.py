@@ -48,7 +48,7 @@ class W4A4WeightsT(ctypes.Structure):
 
 
 class GroupWeightsT(ctypes.Structure):
-    _fields_ = [("N", _i32), ("K", _i32), ("group", _i32), ("flags", _u32), ("codes", _vp), ("scales", _vp)]
+    _fields_ = [("N", _i32), ("K", _i32), ("group", _i32), ("flags", _u32), ("data", _vp)]
 
 
 class KVCacheT(ctypes.Structure):
