@@ -236,7 +236,10 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    (a quantization right before) L2 is where the new values appear.
 
 constexpr int kGemvWarps = 16;
-constexpr int kGemvStages = 8;
+// Tiles that a warp takes in one go: two, whose products do not depend on one another and
+// which share the waiting and counting, unless there is only one.
+constexpr int gemv_pair(int RT) { return RT > 1 ? 2 : 1; }
+constexpr int gemv_stages(int RT) { return 8 / gemv_pair(RT); }
 
 struct GemvArgs {
   const uint16_t *X;
@@ -274,15 +277,16 @@ template <typename T, int GROUP, int RT, int NT>
 __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs a) {
   constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
   constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
-  constexpr int kStage = record_bytes(GROUP);
+  constexpr int kRecord = record_bytes(GROUP), kPair = gemv_pair(RT), kStage = kPair * kRecord;
+  constexpr int kStages = gemv_stages(RT);
   constexpr int kCols = 8 * NT, kTileSums = 16 * kCols;
   constexpr bool kAhead = RT * NT <= 4;             // registers for the next block's tokens
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
   const GroupShape &s = a.s;
-  const uint32_t ring = smem_u32(smem) + warp * kGemvStages * kStage;
-  const int64_t tile_bytes = static_cast<int64_t>(s.blocks) * kStage;
+  const uint32_t ring = smem_u32(smem) + warp * kStages * kStage;
+  const int64_t tile_bytes = static_cast<int64_t>(s.blocks) * kRecord;
   // Tokens r and r + 8 as the B operand; columns behind the last token repeat it
   // (their sums are not used).
   const uint16_t *x_row[NT];
@@ -309,27 +313,33 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
   for (int set = blockIdx.x; set < a.sets; set += gridDim.x) {
     const int tile0 = static_cast<int>(static_cast<int64_t>(set) * s.tiles / a.sets);
     const int tiles = static_cast<int>(static_cast<int64_t>(set + 1) * s.tiles / a.sets) - tile0;
-    // this warp's part of the line
-    const int begin = static_cast<int>(static_cast<int64_t>(warp) * s.blocks * tiles / kGemvWarps);
-    const int end = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks * tiles / kGemvWarps);
-    int kb = begin / tiles, t0 = begin - kb * tiles, left = end - begin;
-    // the copies' place in it: records until the next block of inputs, and in all
-    const int64_t to_next = kStage - (tiles - 1) * tile_bytes;  // from the last tile to the next block's first
-    int copy_t = tiles - t0, copies = left;
+    // this warp's part of the line, in units of kPair tiles
+    const int units = (tiles + kPair - 1) / kPair;
+    const int begin = static_cast<int>(static_cast<int64_t>(warp) * s.blocks * units / kGemvWarps);
+    const int end = static_cast<int>(static_cast<int64_t>(warp + 1) * s.blocks * units / kGemvWarps);
+    int kb = begin / units, u0 = begin - kb * units, left = end - begin;
+    // the copies' place in it: units until the next block of inputs, and in all; an odd last
+    // tile is its own second
+    const int64_t to_next = kRecord - (units - 1) * kPair * tile_bytes;
+    int copy_u = units - u0, copies = left;
     uint32_t copy_dst = ring + 16 * lane;
-    const uint32_t last = ring + (kGemvStages - 1) * kStage;
-    const uint8_t *from = a.data + (tile0 + t0) * tile_bytes + static_cast<int64_t>(kb) * kStage + 16 * lane;
+    const uint32_t last = ring + (kStages - 1) * kStage;
+    const uint8_t *from = a.data + (tile0 + kPair * u0) * tile_bytes + static_cast<int64_t>(kb) * kRecord + 16 * lane;
+    auto second = [&]() { return copy_u == 1 && tiles % 2 ? from : from + tile_bytes; };
     auto advance = [&]() {
-      from += --copy_t ? tile_bytes : to_next;
-      if (copy_t == 0) copy_t = tiles;
+      from += --copy_u ? kPair * tile_bytes : to_next;
+      if (copy_u == 0) copy_u = units;
     };
     if (set == blockIdx.x) {
       const uint8_t *const from0 = from;
-      for (int i = 0; i < min(left, kGemvStages - 1); ++i) {
-        if (128 * lane < kStage) prefetch_l2(from + 112 * lane);  // 128 bytes a lane
+      for (int i = 0; i < min(left, kStages - 1); ++i) {
+        if (128 * lane < kRecord) {  // 128 bytes a lane
+          prefetch_l2(from + 112 * lane);
+          if (kPair == 2) prefetch_l2(second() + 112 * lane);
+        }
         advance();
       }
-      from = from0, copy_t = tiles - t0;
+      from = from0, copy_u = units - u0;
       griddep_wait();
     }
     auto fill = [&]() {
@@ -337,13 +347,19 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
         copy16(copy_dst, from);
         copy16(copy_dst + 512, from + 512);
         if (lane < 2 * kPer) copy16(copy_dst + 1024, from + 1024);
+        if (kPair == 2) {
+          const uint8_t *f = second();
+          copy16(copy_dst + kRecord, f);
+          copy16(copy_dst + kRecord + 512, f + 512);
+          if (lane < 2 * kPer) copy16(copy_dst + kRecord + 1024, f + 1024);
+        }
         copy_dst = copy_dst >= last ? ring + 16 * lane : copy_dst + kStage;
         advance();
       }
       copy_commit();
     };
 #pragma unroll 1
-    for (int i = 0; i < kGemvStages - 1; ++i) fill();
+    for (int i = 0; i < kStages - 1; ++i) fill();
 
     float total[RT][NT][4];
 #pragma unroll
@@ -357,54 +373,65 @@ __global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs
     uint32_t stage = ring + 16 * lane;
     const int steps_at = 1024 + r * kScaleRow - 16 * lane;
     while (left > 0) {
-      const int t1 = min(tiles, t0 + left);  // tiles t0 .. t1 - 1 of block kb
+      const int u1 = min(units, u0 + left);  // units u0 .. u1 - 1 of block kb
       if (kAhead) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[n][j] = ahead[n][j];
-        if (left > t1 - t0) load_x(ahead, kb + 1);
+        if (left > u1 - u0) load_x(ahead, kb + 1);
       } else {
         load_x(x, kb);
       }
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        if (t < t0 || t >= t1) continue;
-        copy_wait<kGemvStages - 2>();
+      for (int u = 0; u < RT / kPair; ++u) {
+        if (u < u0 || u >= u1) continue;
+        copy_wait<kStages - 2>();
         __syncwarp();
         fill();
-        const uint4 w0 = lds16(stage), w1 = lds16(stage + 512);
-        const uint32_t lo[4] = {w0.x, w0.y, w0.z, w0.w}, hi[4] = {w1.x, w1.y, w1.z, w1.w};
-        float part[NT][4];
+        uint4 w[kPair][2];
+#pragma unroll
+        for (int t = 0; t < kPair; ++t) {
+          w[t][0] = lds16(stage + t * kRecord);
+          w[t][1] = lds16(stage + t * kRecord + 512);
+        }
+        float part[kPair][NT][4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t p[4], q[4];
-          T::codes(lo[j], p);
-          T::codes(hi[j], q);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (j % (GROUP / 32) == 0)
-              T::mma0(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
-            else
-              T::mma(part[n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
-            T::mma(part[n], p[2], q[2], p[3], q[3], x[n][j].z, x[n][j].w);
-          }
-          if ((j + 1) % (GROUP / 32) == 0) {
-            const uint32_t steps = lds4(stage + steps_at + 4 * (j / (GROUP / 32)));
-            const float s0 = T::lo(steps), s1 = T::hi(steps);
+          for (int t = 0; t < kPair; ++t) {
+            uint32_t p[4], q[4];
+            T::codes(j == 0 ? w[t][0].x : j == 1 ? w[t][0].y : j == 2 ? w[t][0].z : w[t][0].w, p);
+            T::codes(j == 0 ? w[t][1].x : j == 1 ? w[t][1].y : j == 2 ? w[t][1].z : w[t][1].w, q);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              total[t][n][0] = fmaf(s0, part[n][0], total[t][n][0]);
-              total[t][n][1] = fmaf(s0, part[n][1], total[t][n][1]);
-              total[t][n][2] = fmaf(s1, part[n][2], total[t][n][2]);
-              total[t][n][3] = fmaf(s1, part[n][3], total[t][n][3]);
+              if (j % (GROUP / 32) == 0)
+                T::mma0(part[t][n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
+              else
+                T::mma(part[t][n], p[0], q[0], p[1], q[1], x[n][j].x, x[n][j].y);
+              T::mma(part[t][n], p[2], q[2], p[3], q[3], x[n][j].z, x[n][j].w);
+            }
+          }
+          if ((j + 1) % (GROUP / 32) == 0) {
+#pragma unroll
+            for (int t = 0; t < kPair; ++t) {
+              const uint32_t steps = lds4(stage + t * kRecord + steps_at + 4 * (j / (GROUP / 32)));
+              const float s0 = T::lo(steps), s1 = T::hi(steps);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float(&sum)[4] = total[kPair * u + t][n];
+                sum[0] = fmaf(s0, part[t][n][0], sum[0]);
+                sum[1] = fmaf(s0, part[t][n][1], sum[1]);
+                sum[2] = fmaf(s1, part[t][n][2], sum[2]);
+                sum[3] = fmaf(s1, part[t][n][3], sum[3]);
+              }
             }
           }
         }
         stage = stage >= last ? ring + 16 * lane : stage + kStage;
       }
-      left -= t1 - t0;
-      t0 = 0;
+      left -= u1 - u0;
+      u0 = 0;
       ++kb;
     }
     copy_wait<0>();
@@ -495,7 +522,7 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kRing = kGemvWarps * kGemvStages * record_bytes(GROUP);
+  constexpr int kRing = kGemvWarps * 8 * record_bytes(GROUP);
   constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
   static ContextCache<int> ready;  // per context: attribute set
   int done = 0;
