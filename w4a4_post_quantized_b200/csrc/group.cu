@@ -235,11 +235,13 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    to be brought into L2: those do not depend on that kernel, and where they do
 //    (a quantization right before) L2 is where the new values appear.
 
-constexpr int kGemvWarps = 16;
+// Warps of a block: where two sets of columns double the sums, half as many with twice
+// the registers.
+constexpr int gemv_warps(int RT, int NT) { return RT * NT > 16 ? 8 : 16; }
 // Tiles that a warp takes in one go: two, whose products do not depend on one another and
 // which share the waiting and counting, unless there is only one.
 constexpr int gemv_pair(int RT) { return RT > 1 ? 2 : 1; }
-constexpr int gemv_stages(int RT) { return 8 / gemv_pair(RT); }
+constexpr int gemv_stages(int RT, int NT) { return 128 / gemv_warps(RT, NT) / gemv_pair(RT); }
 
 struct GemvArgs {
   const uint16_t *X;
@@ -274,11 +276,11 @@ __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefe
 
 // GROUP inputs per step, at most RT tiles of 16 rows at a time, NT times 8 tokens.
 template <typename T, int GROUP, int RT, int NT>
-__global__ void __launch_bounds__(32 * kGemvWarps, 1) group_gemv_kernel(GemvArgs a) {
+__global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(GemvArgs a) {
   constexpr int kPer = kBlockK / GROUP;             // groups of a block of inputs
   constexpr int kScaleRow = 4 * kPer;               // bytes of the steps of rows r and r + 8
   constexpr int kRecord = record_bytes(GROUP), kPair = gemv_pair(RT), kStage = kPair * kRecord;
-  constexpr int kStages = gemv_stages(RT);
+  constexpr int kStages = gemv_stages(RT, NT), kGemvWarps = gemv_warps(RT, NT);
   constexpr int kCols = 8 * NT, kTileSums = 16 * kCols;
   constexpr bool kAhead = RT * NT <= 4;             // registers for the next block's tokens
   extern __shared__ __align__(128) uint8_t smem[];
@@ -522,7 +524,7 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kRing = kGemvWarps * 8 * record_bytes(GROUP);
+  constexpr int kGemvWarps = gemv_warps(RT, NT), kRing = 128 * record_bytes(GROUP);
   constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
   static ContextCache<int> ready;  // per context: attribute set
   int done = 0;
@@ -546,7 +548,7 @@ w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
     return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 1>(a, stream) : launch_gemv_t<T, GROUP, 16, 1>(a, stream);
   }
   if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 2>(a, stream);
-  return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 2>(a, stream) : launch_gemv_t<T, GROUP, 8, 2>(a, stream);
+  return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 2>(a, stream) : launch_gemv_t<T, GROUP, 16, 2>(a, stream);
 }
 
 }  // namespace
