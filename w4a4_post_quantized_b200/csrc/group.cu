@@ -71,6 +71,12 @@ __device__ __forceinline__ void quantize_pair(float x0, float x1, unsigned long 
   o1 = __float_as_uint(b + 12582720.0f);
 }
 
+__device__ __forceinline__ float rcp_approx(float x) {  // within 2^-23
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __noinline__ int slow_code(float x, float step) {
   return step > 0.0f ? static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(x, step)), -8.0f), 7.0f)) : 0;
 }
@@ -109,10 +115,12 @@ __global__ void __launch_bounds__(32 * kPackWarps)
       top = T::max2(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = T::max2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const float m = fmaxf(T::lo(top), T::hi(top));
-      const uint16_t step16 = T::round(__fdiv_rn(m, 7.0f));
+      // m / 7: a product is as good, for m has at most 11 bits and no such quotient lies
+      // within 2^-14 of the middle between two 16-bit values
+      const uint16_t step16 = T::round(m * (1.0f / 7.0f));
       const float step = T::to_f32(step16);
       steps[g] = h == 0 ? step16 : steps[g] | (static_cast<uint32_t>(step16) << 16);
-      const float inv = 1.0f / step;
+      const float inv = rcp_approx(step);
       // a step so small that its own rounding, or its reciprocal's range, matters
       const bool plain = step >= 0x1p-100f && m * inv < 7.4f;
 #pragma unroll
