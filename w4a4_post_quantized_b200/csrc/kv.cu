@@ -38,28 +38,34 @@ struct AppendArgs {
   bool pairs;
 };
 
-// Two 16-byte pieces (8 elements each) of a head turned by 8 pairs of angles:
-// elements i of the first with i of the second, or neighbours within each.
+// Pairs of elements turned: (a, b) -> (a c - b s, b c + a s).  Halves: elements i of
+// two 16-byte pieces, with 8 angles; neighbours: within one piece, with 4.
 template <typename T>
-__device__ __forceinline__ void turn(uint4 &x, uint4 &y, const float (&c)[8], const float (&s)[8], bool pairs) {
+__device__ __forceinline__ void turn_halves(uint4 &x, uint4 &y, const float (&c)[8], const float (&s)[8]) {
   uint32_t a[4] = {x.x, x.y, x.z, x.w}, b[4] = {y.x, y.y, y.z, y.w};
-  if (pairs) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = T::lo(a[i]), a1 = T::hi(a[i]), b0 = T::lo(b[i]), b1 = T::hi(b[i]);
-      a[i] = T::pack(a0 * c[i] - a1 * s[i], a1 * c[i] + a0 * s[i]);
-      b[i] = T::pack(b0 * c[i + 4] - b1 * s[i + 4], b1 * c[i + 4] + b0 * s[i + 4]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = T::lo(a[i]), a1 = T::hi(a[i]), b0 = T::lo(b[i]), b1 = T::hi(b[i]);
-      a[i] = T::pack(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
-      b[i] = T::pack(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float a0 = T::lo(a[i]), a1 = T::hi(a[i]), b0 = T::lo(b[i]), b1 = T::hi(b[i]);
+    a[i] = T::pack(a0 * c[2 * i] - b0 * s[2 * i], a1 * c[2 * i + 1] - b1 * s[2 * i + 1]);
+    b[i] = T::pack(b0 * c[2 * i] + a0 * s[2 * i], b1 * c[2 * i + 1] + a1 * s[2 * i + 1]);
   }
   x = make_uint4(a[0], a[1], a[2], a[3]);
   y = make_uint4(b[0], b[1], b[2], b[3]);
+}
+template <typename T, int FIRST>
+__device__ __forceinline__ void turn_neighbours(uint4 &x, const float (&c)[8], const float (&s)[8]) {
+  uint32_t a[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a0 = T::lo(a[i]), a1 = T::hi(a[i]);
+    a[i] = T::pack(a0 * c[FIRST + i] - a1 * s[FIRST + i], a1 * c[FIRST + i] + a0 * s[FIRST + i]);
+  }
+  x = make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+__device__ __forceinline__ void load4(const float *from, float (&to)[8], int first) {
+  const float4 v = *reinterpret_cast<const float4 *>(from);
+  to[first] = v.x, to[first + 1] = v.y, to[first + 2] = v.z, to[first + 3] = v.w;
 }
 
 // ------------------------------------------------------------------- append
@@ -67,11 +73,14 @@ __device__ __forceinline__ void turn(uint4 &x, uint4 &y, const float (&c)[8], co
 // Every byte of the new keys, values and queries is read and written once: bound by
 // HBM for prompts, by the chain position -> page -> store for a few tokens.  A warp
 // takes a token (or one of `parts` shares of its heads, where tokens are too few to
-// fill the GPU).  A lane keeps one unit of 16 elements for good, two pieces that turn
-// together, so the token's cosines and sines are read once into registers, and goes
-// over the heads in rounds of four whose loads are all in flight before the first
-// store, and before the page is known.  (One block per token, thread by
-// thread over its elements, took 67 us for 8 frames.)
+// fill the GPU).  A lane keeps two 16-byte pieces of the heads for good, where halves
+// turn the two that turn together, so the token's cosines and sines are read once into
+// registers, and goes over the heads in rounds of four whose loads are all in flight
+// before the first store, and before the page is known.  The pieces of
+// neighbouring lanes are neighbours in memory: with each lane's two pieces side by side
+// every sector was written in two halves, 24.6 us instead of 22 for 5003 tokens of 128
+// dims turned in part.  (One block per token, thread by thread over its elements, took 67
+// us for 8 frames; now 26, and 94 % of the copy rate on four times as many tokens.)
 constexpr int kAppendWarps = 4;
 
 template <typename T, int D>
@@ -93,20 +102,30 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
   const int entry = p / a.cache.page_size;
   int page = -1;
   if (s >= 0 && s < a.pages.n_seqs && entry < a.pages.max_pages) page = a.pages.table[s * a.pages.max_pages + entry];
-  const bool turned = u < a.rot_dim / 16;
   const bool in_table = a.rot_dim == 0 || (angle >= 0 && angle < a.n_table);
+  // This lane's pieces of a head: elements e0 .. + 7 and e1 .. + 7, and whether they turn.
+  const int half = a.rot_dim / 2;
+  int e0 = 8 * u, e1 = D / 2 + 8 * u;
+  bool turn0, turn1;
   float c[8], sn[8];
-  if (turned && in_table) {
-    const float4 *row = reinterpret_cast<const float4 *>(a.table + angle * a.rot_dim + 8 * u);
-    const float4 *row2 = reinterpret_cast<const float4 *>(a.table + angle * a.rot_dim + a.rot_dim / 2 + 8 * u);
-    const float4 c0 = row[0], c1 = row[1], s0 = row2[0], s1 = row2[1];
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w, c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-    sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
+  const float *cosines = a.table + angle * a.rot_dim;
+  if (a.pairs) {
+    turn0 = e0 < a.rot_dim;
+    turn1 = e1 < a.rot_dim;
+    if (turn0 && in_table) load4(cosines + e0 / 2, c, 0), load4(cosines + half + e0 / 2, sn, 0);
+    if (turn1 && in_table) load4(cosines + e1 / 2, c, 4), load4(cosines + half + e1 / 2, sn, 4);
+  } else {
+    const int units = a.rot_dim / 16;  // lanes u < units turn, the others copy what is left
+    turn0 = turn1 = u < units;
+    e0 = turn0 ? 8 * u : a.rot_dim + 8 * (u - units);
+    e1 = e0 + (turn0 ? half : (D - a.rot_dim) / 2);
+    if (turn0 && in_table) {
+      load4(cosines + e0, c, 0), load4(cosines + e0 + 4, c, 4);
+      load4(cosines + half + e0, sn, 0), load4(cosines + half + e0 + 4, sn, 4);
+    }
   }
-  // heads in the order keys, queries, values; the two pieces of this lane in each
+  // heads in the order keys, queries, values
   const int Hk = a.cache.heads, Hq = a.q_heads, total = 2 * Hk + Hq;
-  const int halves = turned && !a.pairs;
-  const int e0 = halves ? 8 * u : 16 * u, e1 = halves ? a.rot_dim / 2 + 8 * u : 16 * u + 8;
   const int64_t row = page * a.cache.stride_page + (p - entry * a.cache.page_size) * a.cache.stride_token;
   const bool ok = page >= 0 && page < a.cache.n_pages && in_table;
   if (!ok) {
@@ -123,8 +142,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
         const uint16_t *src = h < Hk ? a.k + t * a.k_stride + h * D
                               : value ? a.v + t * a.v_stride + (h - Hk - Hq) * D
                                       : a.q + t * a.q_stride + (h - Hk) * D;
-        x[i] = *reinterpret_cast<const uint4 *>(src + (value ? 16 * u : e0));
-        y[i] = *reinterpret_cast<const uint4 *>(src + (value ? 16 * u + 8 : e1));
+        x[i] = *reinterpret_cast<const uint4 *>(src + (value ? 8 * u : e0));
+        y[i] = *reinterpret_cast<const uint4 *>(src + (value ? D / 2 + 8 * u : e1));
       }
     }
 #pragma unroll
@@ -132,12 +151,19 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
       const int h = h0 + i * kHeads + hl;
       if (h < total) {
         const bool value = h >= Hk + Hq;
-        if (turned && !value) turn<T>(x[i], y[i], c, sn, a.pairs);
+        if (!value) {
+          if (a.pairs) {
+            if (turn0) turn_neighbours<T, 0>(x[i], c, sn);
+            if (turn1) turn_neighbours<T, 4>(y[i], c, sn);
+          } else if (turn0) {
+            turn_halves<T>(x[i], y[i], c, sn);
+          }
+        }
         uint16_t *dst = h < Hk ? a.cache.k + row + h * a.cache.stride_head
                         : value ? a.cache.v + row + (h - Hk - Hq) * a.cache.stride_head
                                 : a.q_out + (t * Hq + (h - Hk)) * D;
-        *reinterpret_cast<uint4 *>(dst + (value ? 16 * u : e0)) = x[i];
-        *reinterpret_cast<uint4 *>(dst + (value ? 16 * u + 8 : e1)) = y[i];
+        *reinterpret_cast<uint4 *>(dst + (value ? 8 * u : e0)) = x[i];
+        *reinterpret_cast<uint4 *>(dst + (value ? D / 2 + 8 * u : e1)) = y[i];
       }
     }
   }
