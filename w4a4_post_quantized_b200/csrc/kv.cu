@@ -304,13 +304,15 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
   const int B = a.pages.n_seqs;
   const int per_seq = a.cache.heads * a.chunks;  // items of a sequence
 
-  // The line of tiles: every thread adds up its run of sequences.
-  const int run = (B + 127) / 128;
+  // The line of tiles.  Up to 32 sequences every warp adds up for itself, one per lane;
+  // of more, every thread of the block adds up a run.
+  const bool few = B <= 32;
+  const int run = few ? 1 : (B + 127) / 128, run0 = few ? lane : tid * run;
   int64_t mine = 0;
-  for (int b = tid * run; b < min(B, (tid + 1) * run); ++b) {
+  for (int i = run0; i < min(B, run0 + run); ++i) {
     int first, end;
     bool over;
-    token_range(a, b, first, end, over);
+    token_range(a, i, first, end, over);
     if (over && blockIdx.x == 0) atomicOr(status, W4A4_DEV_RANGE);
     mine += static_cast<int64_t>((end - first + kTile - 1) / kTile) * per_seq;
   }
@@ -320,20 +322,23 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
-  if (lane == 31) sums[warp] = upto;
-  __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kAttendWarps; ++w) {
-    if (w < warp) upto += sums[w];
-    total += sums[w];
+  int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+  if (!few) {
+    if (lane == 31) sums[warp] = upto;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < kAttendWarps; ++w) {
+      if (w < warp) upto += sums[w];
+      total += sums[w];
+    }
   }
   // Nothing to attend to: zeros, spread over the blocks.
-  for (int b = blockIdx.x; b < B; b += gridDim.x)
-    if (tiles_of(a, b) == 0) {
-      for (int i = tid; i < a.q_heads * D / 8; i += 128)
-        reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(b) * a.q_heads * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = blockIdx.x; i < B; i += gridDim.x)
+    if (tiles_of(a, i) == 0) {
+      for (int j = tid; j < a.q_heads * D / 8; j += 128)
+        reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(i) * a.q_heads * D)[j] = make_uint4(0u, 0u, 0u, 0u);
       if (a.lse)
-        for (int i = tid; i < a.q_heads; i += 128) a.lse[static_cast<int64_t>(b) * a.q_heads + i] = -INFINITY;
+        for (int j = tid; j < a.q_heads; j += 128) a.lse[static_cast<int64_t>(i) * a.q_heads + j] = -INFINITY;
     }
   const int64_t blocks = total < gridDim.x ? total : gridDim.x;  // no share is empty
   if (blockIdx.x >= blocks) {
@@ -344,20 +349,28 @@ __global__ void __launch_bounds__(32 * kAttendWarps) kv_attend_kernel(AttendArgs
   const int64_t share = div_small(total, blocks), more = total - share * blocks;
   const int64_t begin = blockIdx.x * share + min(static_cast<int64_t>(blockIdx.x), more);
   const int64_t stop = begin + share + (blockIdx.x < more ? 1 : 0);
-  if (upto - mine <= begin && begin < upto) {
-    int64_t at = upto - mine;
-    int b = tid * run;
-    for (;; ++b) {
-      const int64_t n = static_cast<int64_t>(tiles_of(a, b)) * per_seq;
-      if (begin < at + n) break;
-      at += n;
+  // the sequence that the share begins in, and where that begins
+  int b;
+  int64_t seq_at;
+  if (few) {
+    b = __ffs(__ballot_sync(0xffffffffu, begin < upto)) - 1;
+    seq_at = __shfl_sync(0xffffffffu, upto - mine, b);
+  } else {
+    if (upto - mine <= begin && begin < upto) {
+      int64_t at = upto - mine;
+      int i = run0;
+      for (;; ++i) {
+        const int64_t n = static_cast<int64_t>(tiles_of(a, i)) * per_seq;
+        if (begin < at + n) break;
+        at += n;
+      }
+      found[0] = at;
+      found[1] = i;
     }
-    found[0] = at;
-    found[1] = b;
+    __syncthreads();
+    seq_at = found[0];
+    b = static_cast<int>(found[1]);
   }
-  __syncthreads();
-  int64_t seq_at = found[0];
-  int b = static_cast<int>(found[1]);
   bool absent = false;
   int4 join = make_int4(-1, 0, 0, 0);
 
