@@ -235,7 +235,10 @@ struct AttendArgs {
   uint16_t *out;
   float *lse;
   float *part;                       // [teams][2][team][chunk][D + 4]: output, maximum, sum
-  int64_t *line;                     // [n_seqs + 1]: where sequences begin in the line, and its length
+
+  // an item's group of heads and chunk
+  __device__ __forceinline__ int heads_of(int item) const { return chunks == 1 ? item : item / chunks; }
+  __device__ __forceinline__ int chunk_of(int item) const { return chunks == 1 ? 0 : item % chunks; }
 };
 
 // Equal shares of the line, the first `more` teams one piece more; none is empty.
@@ -254,13 +257,14 @@ struct Shares {
   }
 };
 
-// The tokens of a sequence, [first, end), and its pieces, [p0, p0 + pieces).
-template <int P>
+// The tokens of a sequence, [first, end), and its pieces, [p0, p0 + pieces).  FRESH: read past
+// L1, where a kernel that has not waited might find what stood there before.
+template <int P, bool FRESH = false>
 struct Range {
   int first, end, p0, pieces;
   __device__ __forceinline__ Range(const AttendArgs &a, int b) {
     const int room = a.pages.max_pages * a.cache.page_size;  // at most 2^30
-    end = min(max(a.lens[b], 0), room);
+    end = min(max(FRESH ? __ldcg(a.lens + b) : a.lens[b], 0), room);
     first = a.window && end > a.window ? end - a.window : 0;
     p0 = first / P;
     pieces = (end + P - 1) / P - p0;
@@ -348,12 +352,11 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     mine += static_cast<int64_t>(v.pieces) * per_seq;
   }
   int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
+  for (int o = 1; o < min(B, 32); o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
-  int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+  int64_t total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
   if (!few) {
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
@@ -362,15 +365,6 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
       if (w < warp) upto += sums[w];
       total += sums[w];
     }
-  }
-  if (blockIdx.x == 0) {  // for the join
-    int64_t at = upto - mine;
-    if (!few || warp == 0)
-      for (int i = run0; i < min(B, run0 + run); ++i) {
-        a.line[i] = at;
-        at += static_cast<int64_t>(Range<P>(a, i).pieces) * per_seq;
-      }
-    if (tid == 0) a.line[B] = total;
   }
   const Shares shares(total, static_cast<int64_t>(gridDim.x) * teams_here);
   const int64_t begin = shares.begin(team);
@@ -445,7 +439,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     page = -1;
     if (a.whole || (t >= cr.first && t < cr.end))
       page = __ldg(a.pages.table + static_cast<int64_t>(cb) * a.pages.max_pages + entry);
-    rest = static_cast<int64_t>(citem / a.chunks * a.team + member) * a.cache.stride_head +
+    rest = static_cast<int64_t>(a.heads_of(citem) * a.team + member) * a.cache.stride_head +
            (t - entry * a.cache.page_size) * a.cache.stride_token;
     look_lo = max(cr.first - look_t0, 0);
     look_hi = min(cr.end - look_t0, P);
@@ -518,8 +512,8 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
       }
     }
     const int n_here = static_cast<int>(min(static_cast<int64_t>(range.pieces - piece), left));
-    const int kvh = item / a.chunks * a.team + member;
-    const int h0 = (item % a.chunks) * a.chunk;            // first head of the chunk, in its group
+    const int kvh = a.heads_of(item) * a.team + member;
+    const int h0 = a.chunk_of(item) * a.chunk;             // first head of the chunk, in its group
     const int heads = min(a.chunk, a.group - h0);
     const int64_t head0 = static_cast<int64_t>(kvh) * a.group + h0;
     const uint16_t *qrow = a.q + b * a.q_stride + head0 * D;
@@ -680,7 +674,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   if (merged) {  // the same for every warp of the block; the rings hold the teams' parts
     __syncthreads();
     const int first = team - team0;                        // this warp joins heads first, first + teams_here, ...
-    const int heads = min(a.chunk, a.group - (item % a.chunks) * a.chunk);
+    const int heads = min(a.chunk, a.group - a.chunk_of(item) * a.chunk);
     for (int h = first; h < heads; h += teams_here) {
       float top = -INFINITY, sum = 0.0f;
       auto part = [&](int t) {
@@ -705,10 +699,11 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 
 // Joins the parts of every item that teams share, per head: a warp per item and head,
 // which leaves at once where one team held all of it; a block where there are more than
-// kManyParts.  Which teams hold parts follows from the line.  A lane takes 4 dims of every
-// kGroups-th part with its own running maximum and sum, 8 parts in flight, so that after
-// the wait two dependent reads remain.  (Lists of the shared items made by every
-// block, or written by the main kernel, cost another one or two; 7 to 11 us in all.)
+// kManyParts.  Which teams hold parts follows from the line, which each block works out
+// while the main kernel still runs.  A lane takes 4 dims of every kGroups-th part with its
+// own running maximum and sum, 8 parts in flight: after the wait one read remains.
+// (Lists of the shared items made by every block, or written by the main kernel, put
+// two or three more behind the wait; 7 to 11 us in all.)
 constexpr int kJoinWarps = 8;
 constexpr int kManyParts = 32;
 
@@ -716,6 +711,7 @@ constexpr int kManyParts = 32;
 // one for every block of teams_here > 1 teams that lies inside it.
 struct Parts {
   int first, left, inner, all, block0, teams_here, first_slot;
+  Parts() = default;
   __device__ __forceinline__ Parts(const Shares &s, int64_t at, int64_t end, int teams_here_) {
     teams_here = teams_here_;
     first = s.owner(at);
@@ -798,68 +794,97 @@ struct Sum {
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(AttendArgs a, int most) {
+  constexpr int P = attend_piece(D);
   constexpr int kPart = D + 4, kLanes = D / 4, kGroups = 32 / kLanes;
+  // a warp's job: its sequence, query head (-1: nothing to do) and parts
+  struct Job {
+    int b, head, h;
+    Parts parts;
+  };
   __shared__ float4 box[kJoinWarps][kLanes];
   __shared__ float2 stats[kJoinWarps];
-  __shared__ int64_t large[kJoinWarps];  // the warps' jobs that take the block
-  griddep_wait();
-  griddep_launch_dependents();
+  __shared__ int64_t starts[32 * kJoinWarps];  // of the runs of sequences in the line
+  __shared__ int64_t sums[kJoinWarps];
+  __shared__ Job large[kJoinWarps];            // the warps' jobs that take the block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = a.pages.n_seqs;
   const int per_seq = a.cache.heads / a.team * a.chunks, per_item = a.team * a.chunk, d = 4 * (lane % kLanes);
   const int64_t slot_floats = static_cast<int64_t>(per_item) * kPart;
-  const int64_t per_b = static_cast<int64_t>(per_seq) * per_item, jobs = a.pages.n_seqs * per_b;
+  const int64_t per_b = static_cast<int64_t>(per_seq) * per_item, jobs = B * per_b;
   const int teams_here = kAttendWarps / a.team;
-  const Shares shares(a.line[a.pages.n_seqs], most);
+  // The line again, from the lengths.  The main kernel does not write them, and lets this one start only when
+  // what was in front of it is done: they can be read before the wait.
+  const int run = (B + 32 * kJoinWarps - 1) / (32 * kJoinWarps);
+  int64_t mine = 0;
+  for (int i = tid * run; i < min(B, (tid + 1) * run); ++i) mine += static_cast<int64_t>(Range<P, true>(a, i).pieces) * per_seq;
+  int64_t upto = mine;
+  for (int o = 1; o < min(B, 32); o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  if (lane == min(B, 32) - 1) sums[warp] = upto;
+  __syncthreads();
+  int64_t total = 0;
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < warp) upto += sums[w];
+    total += sums[w];
+  }
+  starts[tid] = upto - mine;
+  __syncthreads();
+  const Shares shares(total, most);
+  bool waited = false;
   for (int64_t job0 = blockIdx.x; job0 < jobs; job0 += static_cast<int64_t>(gridDim.x) * kJoinWarps) {
     const int64_t job = job0 + static_cast<int64_t>(warp) * gridDim.x;
+    Job v;
+    v.head = -1;
     bool many = false;
-    // this job's sequence, query head (-1: none), parts and place of them
-    auto resolve = [&](int64_t job_, int &b, int &head, int64_t &at, int64_t &end, int &h) {
-      b = static_cast<int>(div_small(job_, per_b));
-      const int in = static_cast<int>(job_ - b * per_b), item = in / per_item;
-      h = in % per_item;
-      const int h0 = (item % a.chunks) * a.chunk, hc = h % a.chunk;
-      head = hc >= min(a.chunk, a.group - h0) ? -1 : (item / a.chunks * a.team + h / a.chunk) * a.group + h0 + hc;
-      const int64_t pieces = Range<attend_piece(D)>(a, b).pieces;
-      at = a.line[b] + item * pieces;
-      end = at + pieces;
-    };
     if (job < jobs) {
-      int b, head, h;
-      int64_t at, end;
-      resolve(job, b, head, at, end, h);
-      if (head >= 0 && end > at) {
-        const Parts parts(shares, at, end, teams_here);
-        many = parts.all > kManyParts;
+      v.b = static_cast<int>(div_small(job, per_b));
+      const int in = static_cast<int>(job - v.b * per_b), item = in / per_item;
+      v.h = in - item * per_item;
+      const int h0 = a.chunk_of(item) * a.chunk, hm = v.h / a.chunk, hc = v.h - hm * a.chunk;
+      const int64_t pieces = Range<P, true>(a, v.b).pieces;
+      if (hc < min(a.chunk, a.group - h0) && pieces > 0) {
+        const int r = v.b / run;
+        int64_t at = starts[r] + item * pieces;
+        for (int i = r * run; i < v.b; ++i) at += static_cast<int64_t>(Range<P, true>(a, i).pieces) * per_seq;
+        v.parts = Parts(shares, at, at + pieces, teams_here);
         // one team held all of it and has written it, unless its block left it as a part
-        if (!many && (parts.all > 1 || parts.inner > 0)) {
-          Sum<D> s;
-          s.gather(a.part + h * kPart, slot_floats, parts, lane / kLanes, kGroups, d);
-          if (lane < kLanes) write_out<T, D>(a, b, head, d, s.o, s.m, s.sum);
-        }
+        if (v.parts.all > 1 || v.parts.inner > 0) v.head = (a.heads_of(item) * a.team + hm) * a.group + h0 + hc;
+        many = v.head >= 0 && v.parts.all > kManyParts;
       }
     }
-    if (lane == 0) large[warp] = many ? job : -1;
+    if (!waited) {
+      griddep_wait();
+      griddep_launch_dependents();
+      waited = true;
+    }
+    if (v.head >= 0 && !many) {
+      Sum<D> s;
+      s.gather(a.part + v.h * kPart, slot_floats, v.parts, lane / kLanes, kGroups, d);
+      if (lane < kLanes) write_out<T, D>(a, v.b, v.head, d, s.o, s.m, s.sum);
+    }
+    if (lane == 0) {
+      if (!many) v.head = -1;
+      large[warp] = v;
+    }
     if (!__syncthreads_or(many)) continue;
     for (int w = 0; w < kJoinWarps; ++w) {
-      if (large[w] < 0) continue;
-      int b, head, h;
-      int64_t at, end;
-      resolve(large[w], b, head, at, end, h);
-      const Parts parts(shares, at, end, teams_here);
+      if (large[w].head < 0) continue;
+      const Job j = large[w];
       Sum<D> s;
-      s.gather(a.part + h * kPart, slot_floats, parts, warp * kGroups + lane / kLanes, kJoinWarps * kGroups, d);
+      s.gather(a.part + j.h * kPart, slot_floats, j.parts, warp * kGroups + lane / kLanes, kJoinWarps * kGroups, d);
       if (lane < kLanes) box[warp][lane] = s.o;
       if (lane == 0) stats[warp] = make_float2(s.m, s.sum);
       __syncthreads();
       if (tid < kLanes) {
         Sum<D> t;
-        float4 v[kJoinWarps];
+        float4 v4[kJoinWarps];
         float2 ml[kJoinWarps];
 #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) v[i] = box[i][tid], ml[i] = stats[i];
-        t.add(v, ml);
-        write_out<T, D>(a, b, head, d, t.o, t.m, t.sum);
+        for (int i = 0; i < kJoinWarps; ++i) v4[i] = box[i][tid], ml[i] = stats[i];
+        t.add(v4, ml);
+        write_out<T, D>(a, j.b, j.head, d, t.o, t.m, t.sum);
       }
       __syncthreads();
     }
@@ -938,10 +963,11 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   if (grid < 1) grid = 1;
   const int teams = static_cast<int>(grid) * teams_here;
   cudaLaunchAttribute attr;
-  // Not before the kernel in front is done: blocks that wait beside the join of the call
-  // before take places that others need, and then not all of them find one at
-  // once (64 sequences of 8k: 155 us in a row of calls, 129 without).
-  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr, false);
+  // Where every place is needed, not before the kernel in front is done: blocks that
+  // wait beside the join of the call before keep others from finding one at once (64
+  // sequences of 8k: 155 us in a row of calls, 129 without).
+  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr,
+                                         2 * grid <= static_cast<int64_t>(device_sm_count()) * per_sm);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
   // one team, or items of one piece: nothing is shared
   if (e != cudaSuccess || teams == 1 || pieces <= 1) return launch_status(e);
@@ -1033,8 +1059,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int6
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
   if (n_seqs < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
     return 0;
-  return w4a4::part_bytes(n_q_heads / n_kv_heads, head_dim) +
-         sizeof(int64_t) * (static_cast<size_t>(n_seqs) + 1);
+  return w4a4::part_bytes(n_q_heads / n_kv_heads, head_dim);
 }
 
 w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_heads, const w4a4_kv_cache_t *cache,
@@ -1074,7 +1099,6 @@ w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_head
   a.out = out;
   a.lse = lse;
   a.part = static_cast<float *>(workspace);
-  a.line = reinterpret_cast<int64_t *>(static_cast<uint8_t *>(workspace) + part_bytes(a.group, D));
   const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0, wide = a.chunk > 8;
   if (D == 64) {
     if (fp16) return wide ? launch_attend<Fp16, 64, 2>(a, stream) : launch_attend<Fp16, 64, 1>(a, stream);
