@@ -164,7 +164,8 @@ size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t
  *   the sum of exponentials) or NULL; pages [n_seqs, max_pages]; lens [n_seqs].
  *   - Rows of a page at or behind the length are never used, whatever they
  *     hold.  Pages may be shared between sequences.
- *   - max_pages * page_size is at most 2^30 (W4A4_ERR_SHAPE above).
+ *   - max_pages * page_size is at most 2^30, and n_seqs * n_q_heads * max_pages *
+ *     page_size / 16 below 2^31 at the least (W4A4_ERR_SHAPE above).
  *   - A length above max_pages * page_size counts as that many, and a row whose
  *     page number is out of range as absent; both set W4A4_DEV_RANGE.
  *   - workspace: at least w4a4_kv_attend_workspace_bytes bytes, contents

@@ -176,7 +176,8 @@ def test_attend_argument_checks(lib):
     for kw, want in BAD_CACHES:
         assert f(_cache(**kw), n_seqs=0) == want, kw
     for kw in (dict(hq=0), dict(hq=9), dict(hq=1 << 16), dict(window=-1), dict(n_seqs=-1), dict(qs=504),
-               dict(wb=need - 1), dict(cache=_cache(page_size=1 << 29), max_pages=3), dict(n_seqs=1 << 16, max_pages=1 << 15, wb=1 << 40)):
+               dict(wb=need - 1), dict(cache=_cache(page_size=1 << 29), max_pages=3),
+               dict(cache=_cache(page_size=1 << 28), max_pages=4, n_seqs=32), dict(n_seqs=1 << 16, max_pages=1 << 15, wb=1 << 40)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(q=None), dict(lens=None), dict(out=None), dict(ws=None), dict(pages=None),
                dict(scale=math.nan), dict(scale=math.inf)):

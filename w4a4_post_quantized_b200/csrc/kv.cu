@@ -212,12 +212,6 @@ constexpr int kChunk = 16;           // most query heads of a warp's item
 constexpr int attend_piece(int D) { return D == 64 ? 32 : 16; }  // tokens of a stage: 8 KB of keys and values
 constexpr int attend_stages(int D, int NT) { return D == 64 ? 2 : 2; }
 
-// a / b without the cost of a 64-bit division where 32 bits do
-__device__ __forceinline__ int64_t div_small(int64_t a, int64_t b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
 struct AttendArgs {
   Cache cache;
   Pages pages;
@@ -241,19 +235,20 @@ struct AttendArgs {
   __device__ __forceinline__ int chunk_of(int item) const { return chunks == 1 ? 0 : item % chunks; }
 };
 
-// Equal shares of the line, the first `more` teams one piece more; none is empty.
+// Equal shares of the line, the first `more` teams one piece more; none is empty.  (Places in
+// the line are below 2^31, checked on the host: a 64-bit division takes half a microsecond.)
 struct Shares {
-  int64_t teams, share, more;
-  __device__ __forceinline__ Shares(int64_t total, int64_t most) {
+  int teams, share, more;
+  __device__ __forceinline__ Shares(int total, int most) {
     teams = min(total, most);
-    share = teams ? div_small(total, teams) : 0;
+    share = teams ? total / teams : 0;
     more = total - share * teams;
   }
-  __device__ __forceinline__ int64_t begin(int64_t team) const { return team * share + min(team, more); }
+  __device__ __forceinline__ int begin(int team) const { return min(team, teams) * share + min(team, more); }
   // the team that holds a place in the line
-  __device__ __forceinline__ int owner(int64_t at) const {
-    const int64_t wide = more * (share + 1);
-    return static_cast<int>(at < wide ? div_small(at, share + 1) : more + div_small(at - wide, share));
+  __device__ __forceinline__ int owner(int at) const {
+    const int wide = more * (share + 1);
+    return at < wide ? at / (share + 1) : more + (at - wide) / share;
   }
 };
 
@@ -330,8 +325,8 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   constexpr int kPart = D + 4;                // floats of a partial result
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint32_t live_rows[kAttendWarps][kStages];
-  __shared__ int64_t sums[kAttendWarps];
-  __shared__ int64_t found[kAttendWarps][2];  // start of the sequence that a team's share begins in, its number
+  __shared__ int sums[kAttendWarps];
+  __shared__ int found[kAttendWarps][2];  // start of the sequence that a team's share begins in, its number
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -345,18 +340,18 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   // of more, every thread of the block adds up a run.
   const bool few = B <= 32;
   const int run = few ? 1 : (B + 127) / 128, run0 = few ? lane : tid * run;
-  int64_t mine = 0;
+  int mine = 0;
   for (int i = run0; i < min(B, run0 + run); ++i) {
     const Range<P> v(a, i);
     if (blockIdx.x == 0 && a.lens[i] > v.end) atomicOr(status, W4A4_DEV_RANGE);
-    mine += static_cast<int64_t>(v.pieces) * per_seq;
+    mine += v.pieces * per_seq;
   }
-  int64_t upto = mine;
+  int upto = mine;
   for (int o = 1; o < min(B, 32); o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
-  int64_t total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
+  int total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
   if (!few) {
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
@@ -366,12 +361,12 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
       total += sums[w];
     }
   }
-  const Shares shares(total, static_cast<int64_t>(gridDim.x) * teams_here);
-  const int64_t begin = shares.begin(team);
-  int64_t left = team < shares.teams ? shares.begin(team + 1) - begin : 0;
+  const Shares shares(total, gridDim.x * teams_here);
+  const int begin = shares.begin(team);
+  int left = team < shares.teams ? shares.begin(team + 1) - begin : 0;
   // The sequence that the share begins in, and where that begins.
   int b = 0;
-  int64_t off = 0;  // of the share in it
+  int off = 0;  // of the share in it
   if (few) {
     if (left) {
       b = __ffs(__ballot_sync(0xffffffffu, begin < upto)) - 1;
@@ -379,12 +374,12 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     }
   } else {
     for (int t = 0; t < teams_here; ++t) {
-      const int64_t from = shares.begin(blockIdx.x * teams_here + t);
+      const int from = shares.begin(blockIdx.x * teams_here + t);
       if (upto - mine <= from && from < upto) {
-        int64_t at = upto - mine;
+        int at = upto - mine;
         int i = run0;
         for (;; ++i) {
-          const int64_t n = static_cast<int64_t>(Range<P>(a, i).pieces) * per_seq;
+          const int n = Range<P>(a, i).pieces * per_seq;
           if (from < at + n) break;
           at += n;
         }
@@ -395,7 +390,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     __syncthreads();
     if (left) {
       off = begin - found[warp / a.team][0];
-      b = static_cast<int>(found[warp / a.team][1]);
+      b = found[warp / a.team][1];
     }
   }
   // Nothing to attend to: zeros, spread over the warps.
@@ -410,9 +405,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 
   // ---- the copies' side: the next piece to look up, then its rows
   Range<P> cr(a, b);
-  int cb = b, citem = static_cast<int>(div_small(off, cr.pieces));
-  int cpiece = static_cast<int>(off - static_cast<int64_t>(citem) * cr.pieces);
-  int64_t cleft = left;
+  int cb = b, citem = off / cr.pieces, cpiece = off - citem * cr.pieces, cleft = left;
   int item = citem, piece = cpiece;            // the products' side starts there too
   Range<P> range = cr;
   const int64_t values = a.cache.v - a.cache.k;
@@ -497,7 +490,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   // ---- the products' side
   // Where the block has several teams and all of them work on one item, they leave one part.
   const int team0 = blockIdx.x * teams_here;
-  const int64_t item_at = begin - piece;
+  const int item_at = begin - piece;
   const bool merged = teams_here > 1 && team0 + teams_here <= shares.teams && item_at <= shares.begin(team0) &&
                       shares.begin(team0 + teams_here) <= item_at + range.pieces;
   int stage = 0;
@@ -511,7 +504,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
         while (range.pieces == 0);
       }
     }
-    const int n_here = static_cast<int>(min(static_cast<int64_t>(range.pieces - piece), left));
+    const int n_here = min(range.pieces - piece, left);
     const int kvh = a.heads_of(item) * a.team + member;
     const int h0 = a.chunk_of(item) * a.chunk;             // first head of the chunk, in its group
     const int heads = min(a.chunk, a.group - h0);
@@ -699,7 +692,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 
 // Joins the parts of every item that teams share, per head: a warp per item and head,
 // which leaves at once where one team held all of it; a block where there are more than
-// kManyParts.  Which teams hold parts follows from the line, which each block works out
+// kManyParts (a quarter as many where every block has one job at most).  Which teams hold parts follows from the line, which each block works out
 // while the main kernel still runs.  A lane takes 4 dims of every kGroups-th part with its
 // own running maximum and sum, 8 parts in flight: after the wait one read remains.
 // (Lists of the shared items made by every block, or written by the main kernel, put
@@ -712,7 +705,7 @@ constexpr int kManyParts = 32;
 struct Parts {
   int first, left, inner, all, block0, teams_here, first_slot;
   Parts() = default;
-  __device__ __forceinline__ Parts(const Shares &s, int64_t at, int64_t end, int teams_here_) {
+  __device__ __forceinline__ Parts(const Shares &s, int at, int end, int teams_here_) {
     teams_here = teams_here_;
     first = s.owner(at);
     const int last = s.owner(end - 1);
@@ -803,28 +796,30 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(AttendArgs a, 
   };
   __shared__ float4 box[kJoinWarps][kLanes];
   __shared__ float2 stats[kJoinWarps];
-  __shared__ int64_t starts[32 * kJoinWarps];  // of the runs of sequences in the line
-  __shared__ int64_t sums[kJoinWarps];
+  __shared__ int starts[32 * kJoinWarps];  // of the runs of sequences in the line
+  __shared__ int sums[kJoinWarps];
   __shared__ Job large[kJoinWarps];            // the warps' jobs that take the block
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.pages.n_seqs;
   const int per_seq = a.cache.heads / a.team * a.chunks, per_item = a.team * a.chunk, d = 4 * (lane % kLanes);
   const int64_t slot_floats = static_cast<int64_t>(per_item) * kPart;
-  const int64_t per_b = static_cast<int64_t>(per_seq) * per_item, jobs = B * per_b;
+  const int per_b = per_seq * per_item;
+  const int64_t jobs = static_cast<int64_t>(B) * per_b;
+  const int many_parts = jobs <= gridDim.x ? kManyParts / 4 : kManyParts;
   const int teams_here = kAttendWarps / a.team;
   // The line again, from the lengths.  The main kernel does not write them, and lets this one start only when
   // what was in front of it is done: they can be read before the wait.
   const int run = (B + 32 * kJoinWarps - 1) / (32 * kJoinWarps);
-  int64_t mine = 0;
-  for (int i = tid * run; i < min(B, (tid + 1) * run); ++i) mine += static_cast<int64_t>(Range<P, true>(a, i).pieces) * per_seq;
-  int64_t upto = mine;
+  int mine = 0;
+  for (int i = tid * run; i < min(B, (tid + 1) * run); ++i) mine += Range<P, true>(a, i).pieces * per_seq;
+  int upto = mine;
   for (int o = 1; o < min(B, 32); o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    const int v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
   if (lane == min(B, 32) - 1) sums[warp] = upto;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
   for (int w = 0; w < kJoinWarps; ++w) {
     if (w < warp) upto += sums[w];
     total += sums[w];
@@ -839,19 +834,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(AttendArgs a, 
     v.head = -1;
     bool many = false;
     if (job < jobs) {
-      v.b = static_cast<int>(div_small(job, per_b));
-      const int in = static_cast<int>(job - v.b * per_b), item = in / per_item;
+      v.b = jobs < (int64_t(1) << 31) ? static_cast<int>(job) / per_b : static_cast<int>(job / per_b);
+      const int in = static_cast<int>(job - static_cast<int64_t>(v.b) * per_b), item = in / per_item;
       v.h = in - item * per_item;
       const int h0 = a.chunk_of(item) * a.chunk, hm = v.h / a.chunk, hc = v.h - hm * a.chunk;
-      const int64_t pieces = Range<P, true>(a, v.b).pieces;
+      const int pieces = Range<P, true>(a, v.b).pieces;
       if (hc < min(a.chunk, a.group - h0) && pieces > 0) {
         const int r = v.b / run;
-        int64_t at = starts[r] + item * pieces;
-        for (int i = r * run; i < v.b; ++i) at += static_cast<int64_t>(Range<P, true>(a, i).pieces) * per_seq;
+        int at = starts[r] + item * pieces;
+        for (int i = r * run; i < v.b; ++i) at += Range<P, true>(a, i).pieces * per_seq;
         v.parts = Parts(shares, at, at + pieces, teams_here);
         // one team held all of it and has written it, unless its block left it as a part
         if (v.parts.all > 1 || v.parts.inner > 0) v.head = (a.heads_of(item) * a.team + hm) * a.group + h0 + hc;
-        many = v.head >= 0 && v.parts.all > kManyParts;
+        many = v.head >= 0 && v.parts.all > many_parts;
       }
     }
     if (!waited) {
@@ -950,7 +945,6 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
     return W4A4_ERR_CUDA;
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
-  a.team = a.cache.heads % 4 == 0 ? 4 : a.cache.heads % 2 == 0 ? 2 : 1;
   a.whole = a.cache.page_size % P == 0;
   // blocks: one per place on the GPU, fewer when there cannot be that many pieces
   const int teams_here = kAttendWarps / a.team;
@@ -1090,6 +1084,12 @@ w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_head
   a.group = n_q_heads / a.cache.heads;
   a.chunks = (a.group + kChunk - 1) / kChunk;
   a.chunk = (a.group + a.chunks - 1) / a.chunks;
+  a.team = a.cache.heads % 4 == 0 ? 4 : a.cache.heads % 2 == 0 ? 2 : 1;
+  {  // the line of pieces is counted in 32 bits
+    const int64_t pieces = (static_cast<int64_t>(max_pages) * a.cache.page_size + 15) / 16;
+    const int64_t items = static_cast<int64_t>(a.cache.heads / a.team) * a.chunks;
+    if (items * pieces >= (int64_t(1) << 31) / n_seqs) return W4A4_ERR_SHAPE;
+  }
   int shift = 0;  // page_size <= 2^shift
   while ((int64_t(1) << shift) < a.cache.page_size) ++shift;
   a.div_shift = 31 + shift;
