@@ -142,7 +142,7 @@ w4a4_status w4a4_rope_table(int32_t n_pos, int32_t rot_dim, double base, float *
  *     over more than one) is refused (W4A4_ERR_SHAPE).
  *   - Strides are multiples of 8 elements, at least n_heads * head_dim
  *     (q: n_q_heads * head_dim).  rot_dim: a multiple of 16, at most head_dim.
- *     T < 2^31; n_seqs * max_pages < 2^31. */
+ *     T < 2^31; n_seqs <= 2^24; n_seqs * max_pages < 2^31. */
 w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int64_t k_stride, const uint16_t *v,
                            int64_t v_stride, const uint16_t *q, int64_t q_stride, int32_t n_q_heads,
                            uint16_t *q_out, int64_t T, const int32_t *pages, int32_t n_seqs, int32_t max_pages,

@@ -148,6 +148,7 @@ def test_append_argument_checks(lib):
     for kw in (dict(stride_page=0), dict(stride_token=0), dict(stride_head=0)):
         assert f(_cache(**kw)) == SHAPE
     for kw in (dict(T=-1), dict(T=1 << 31), dict(n_table=-1), dict(hq=0), dict(n_seqs=-1), dict(max_pages=-1),
+               dict(n_seqs=(1 << 24) + 1, max_pages=1),
                dict(n_seqs=1 << 16, max_pages=1 << 15), dict(ks=248), dict(vs=0), dict(qs=504)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(k=None), dict(v=None), dict(pos=None), dict(qo=None), dict(table=None), dict(pages=None),

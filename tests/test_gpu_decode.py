@@ -449,6 +449,28 @@ def test_attend_long_and_many(w4, B, L, Hq, H, D, dt):
     check_attend(w4, *attend_case(w4, B, lens, Hq, H, D, 64, "hnd", dt, L))
 
 
+@pytest.mark.parametrize("seed", range(24))
+def test_attend_drawn(w4, seed):
+    """Drawn batches: the line of pieces is cut at ever other places, into parts of
+    single warps and of whole blocks."""
+    g = gen(1000 + seed)
+    pick = lambda *v: v[int(torch.randint(0, len(v), (1,), generator=g))]
+    B, H, G = pick(1, 2, 3, 7, 31, 33, 60), pick(1, 2, 3, 4, 6, 8), pick(1, 2, 3, 8, 9, 17)
+    top = pick(3, 40, 700, 4000)
+    lens = torch.randint(0, top + 1, (B,), generator=g).tolist()
+    lens[int(torch.randint(0, B, (1,), generator=g))] = top * pick(1, 5)
+    D, page = pick(64, 128), pick(1, 5, 16, 32, 48, 64)
+    case = attend_case(w4, B, lens, G * H, H, D, page, pick("nhd", "hnd", "gaps"), pick(BF16, FP16), seed)
+    check_attend(w4, *case, window=pick(0, 0, 13, 64, 1000))
+
+
+def test_attend_very_many(w4):
+    """More sequences than threads: every thread adds up a run of them."""
+    lens = [(i * i) % 23 if i % 7 else 0 for i in range(1500)]
+    lens[1400] = 3000
+    check_attend(w4, *attend_case(w4, 1500, lens, 4, 2, 64, 16, "nhd", BF16, 77))
+
+
 def test_attend_one_long_among_many_short(w4):
     check_attend(w4, *attend_case(w4, 40, [20_011 if i == 17 else i % 3 for i in range(40)], 8, 4, 64, 16, "nhd", BF16, 3))
 
@@ -678,6 +700,27 @@ def test_on_another_stream(w4):
             close(got, o, ob, BF16)
         for y in ys:
             close(y, want, bound, BF16)
+
+
+def test_two_calls_at_once(w4):
+    """Calls on two streams, each with a workspace of its own, while a third appends elsewhere."""
+    cases = [attend_case(w4, 2, [9000, 4000], 8, 4, 64, 16, "nhd", BF16, 71),
+             attend_case(w4, 3, [100, 7000, 3], 16, 1, 128, 64, "hnd", BF16, 72)]
+    args = [(c[0].cuda(), c[1], c[4].cuda(), c[5].cuda()) for c in cases]
+    want = [w4.w4a4_kv_attend(*a) for a in args]
+    X, w, b, _, _ = gemv_case(w4, 16, 700, 4096, 64, BF16, True, 73)
+    y = w4.w4a4_group_gemv(X, w, b)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = [[], [], []]
+    for _ in range(20):
+        for i in range(2):
+            outs[i].append(w4.w4a4_kv_attend(*args[i], stream=streams[i]))
+        outs[2].append(w4.w4a4_group_gemv(X, w, b, stream=streams[2]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+    assert all(torch.equal(o, y) for o in outs[2])
 
 
 def test_refusals_of_the_binding(w4):
