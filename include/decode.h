@@ -124,57 +124,74 @@ typedef struct {
  * frequencies) are tables of the caller's own. */
 w4a4_status w4a4_rope_table(int32_t n_pos, int32_t rot_dim, double base, float *table);
 
-/* T new tokens enter the cache: token t with keys k[t] and values v[t] ([n_heads,
- * head_dim], tokens k_stride / v_stride elements apart) becomes position pos[t]
- * of sequence seq[t] (NULL: sequence t), which lives in page pages[seq,
- * pos / page_size] (pages [n_seqs, max_pages] int32) at row pos % page_size.
- * Keys, and queries q[t] ([n_q_heads, head_dim], q_stride apart; q may be NULL)
- * on their way to q_out ([T, n_q_heads, head_dim], contiguous; may be q itself when
- * q_stride = n_q_heads * head_dim, must not overlap it otherwise), are rotated:
- * with (a, b) elements i and i + rot_dim / 2 (W4A4_FLAG_ROPE_PAIRS: 2i and 2i + 1)
- * of a head and (c, s) elements i and i + rot_dim / 2 of row table_pos[t] (NULL:
- * pos[t]) of table [n_table, rot_dim] fp32, a' = a c - b s, b' = b c + a s in
- * fp32, rounded once; elements from rot_dim on, values, and everything when
- * rot_dim = 0 (table may then be NULL) are copied.
+/* New tokens for w4a4_kv_append.  Strides are in elements. */
+typedef struct {
+    const uint16_t *k, *v;    /* [n_tokens, n_heads, head_dim], tokens k_stride / v_stride apart */
+    const uint16_t *q;        /* [n_tokens, n_q_heads, head_dim], q_stride apart; or NULL */
+    uint16_t *q_out;          /* [n_tokens, n_q_heads, head_dim], contiguous (with q) */
+    int64_t k_stride, v_stride, q_stride;
+    int64_t n_tokens;
+    const int32_t *pages;     /* [n_seqs, max_pages] page numbers */
+    const int32_t *seq;       /* [n_tokens] sequence of each token; NULL: token t is sequence t */
+    const int32_t *pos;       /* [n_tokens] position of each token in its sequence */
+    const int32_t *table_pos; /* [n_tokens] row of the table; NULL: pos */
+    const float *table;       /* [n_table, rot_dim] cosines, then sines; NULL when rot_dim = 0 */
+    int32_t n_seqs, max_pages, n_q_heads, n_table, rot_dim;
+    uint32_t flags;           /* 0 or W4A4_FLAG_ROPE_PAIRS */
+} w4a4_kv_append_t;
+
+/* New tokens enter the cache: token t with keys k[t] and values v[t] becomes position pos[t]
+ * of sequence seq[t], which lives in page pages[seq, pos / page_size] at row pos %
+ * page_size.  Keys, and queries on their way from q to q_out (which may be q itself when
+ * q_stride = n_q_heads * head_dim, and must not overlap it otherwise), are rotated: with
+ * (a, b) elements i and i + rot_dim / 2 (W4A4_FLAG_ROPE_PAIRS: 2i and 2i + 1) of a head and
+ * (c, s) elements i and i + rot_dim / 2 of the token's row of the table, a' = a c - b s, b' =
+ * b c + a s in fp32, rounded once; elements from rot_dim on, values, and everything when
+ * rot_dim = 0 are copied.
  *   - A negative pos[t] marks a padding token: nothing of it is read or written.
  *   - Two tokens of one call must not name the same row of a page: which one stays is
  *     not defined.  A cache whose pages, rows or heads share memory (a stride of 0
  *     over more than one) is refused (W4A4_ERR_SHAPE).
- *   - Strides are multiples of 8 elements, at least n_heads * head_dim
- *     (q: n_q_heads * head_dim).  rot_dim: a multiple of 16, at most head_dim.
- *     T < 2^31; n_seqs <= 2^24; n_seqs * max_pages < 2^31. */
-w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int64_t k_stride, const uint16_t *v,
-                           int64_t v_stride, const uint16_t *q, int64_t q_stride, int32_t n_q_heads,
-                           uint16_t *q_out, int64_t T, const int32_t *pages, int32_t n_seqs, int32_t max_pages,
-                           const int32_t *seq, const int32_t *pos, const float *table, int32_t n_table,
-                           int32_t rot_dim, const int32_t *table_pos, uint32_t flags, void *stream);
+ *   - Strides are multiples of 8, at least n_heads * head_dim (q: n_q_heads * head_dim).
+ *     rot_dim: a multiple of 16, at most head_dim.  n_tokens < 2^31; n_seqs <= 2^24; n_seqs *
+ *     max_pages < 2^31. */
+w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t *tokens, void *stream);
 
 /* Device workspace of w4a4_kv_attend: 0 for arguments that it does not accept. */
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim);
+
+/* One new token per sequence for w4a4_kv_attend. */
+typedef struct {
+    const uint16_t *q;        /* [n_seqs, n_q_heads, head_dim], sequences q_stride elements apart */
+    uint16_t *out;            /* [n_seqs, n_q_heads, head_dim], contiguous */
+    float *lse;               /* [n_seqs, n_q_heads] logarithm of the sum of exponentials, or NULL */
+    void *workspace;          /* w4a4_kv_attend_workspace_bytes bytes, contents irrelevant */
+    const int32_t *pages;     /* [n_seqs, max_pages] page numbers */
+    const int32_t *lens;      /* [n_seqs] tokens of each sequence */
+    int64_t q_stride;         /* a multiple of 8 */
+    size_t workspace_bytes;
+    int32_t n_seqs, max_pages;
+    int32_t n_q_heads;        /* a multiple of the cache's n_heads */
+    int32_t window;           /* attend to the last `window` tokens; 0: to all */
+    float scale;
+} w4a4_kv_attend_t;
 
 /* One new token of every sequence against its cache: for sequence b and query
  * head h, which reads cache head h / (n_q_heads / n_heads),
  *   out[b, h] = sum_t p_t V[t],  p = softmax_t(scale * q[b, h] . K[t])
  * over positions t in [max(0, lens[b] - window), lens[b]) (window 0: all).
  * Statistics and sums are fp32; the result is rounded once.  A sequence
- * with nothing to attend to (length 0 or negative) gets zeros, and lse = -inf.
- *   q [n_seqs, n_q_heads, head_dim], sequences q_stride elements apart (a multiple
- *   of 8); n_q_heads a multiple of cache->n_heads; out [n_seqs, n_q_heads,
- *   head_dim] contiguous; lse [n_seqs, n_q_heads] fp32 (natural logarithm of
- *   the sum of exponentials) or NULL; pages [n_seqs, max_pages]; lens [n_seqs].
+ * with nothing to attend to (length 0 or negative), or all of whose scores are -inf, gets
+ * zeros, and lse = -inf.
  *   - Rows of a page at or behind the length are never used, whatever they
  *     hold.  Pages may be shared between sequences.
- *   - max_pages * page_size is at most 2^30, and n_seqs * n_q_heads * max_pages *
- *     page_size / 16 below 2^31 at the least (W4A4_ERR_SHAPE above).
+ *   - max_pages * page_size is at most 2^30, n_seqs at most 2^24, and n_seqs * n_q_heads *
+ *     max_pages * page_size / 16 below 2^31 at the least (W4A4_ERR_SHAPE above).
  *   - A length above max_pages * page_size counts as that many, and a row whose
  *     page number is out of range as absent; both set W4A4_DEV_RANGE.
- *   - workspace: at least w4a4_kv_attend_workspace_bytes bytes, contents
- *     irrelevant; calls that may overlap on the GPU need one each.
+ *   - Calls that may overlap on the GPU need a workspace each.
  *   - The same inputs give the same bits on every call on one GPU. */
-w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_heads, const w4a4_kv_cache_t *cache,
-                           const int32_t *pages, int32_t n_seqs, int32_t max_pages, const int32_t *lens,
-                           float scale, int32_t window, uint16_t *out, float *lse, void *workspace,
-                           size_t workspace_bytes, void *stream);
+w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t *tokens, void *stream);
 
 #ifdef __cplusplus
 }

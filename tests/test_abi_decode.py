@@ -26,6 +26,19 @@ class CacheT(ctypes.Structure):
                 ("flags", u32), ("stride_page", i64), ("stride_token", i64), ("stride_head", i64)]
 
 
+class AppendT(ctypes.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("q", vp), ("q_out", vp), ("k_stride", i64), ("v_stride", i64),
+                ("q_stride", i64), ("n_tokens", i64), ("pages", vp), ("seq", vp), ("pos", vp), ("table_pos", vp),
+                ("table", vp), ("n_seqs", i32), ("max_pages", i32), ("n_q_heads", i32), ("n_table", i32),
+                ("rot_dim", i32), ("flags", u32)]
+
+
+class AttendT(ctypes.Structure):
+    _fields_ = [("q", vp), ("out", vp), ("lse", vp), ("workspace", vp), ("pages", vp), ("lens", vp),
+                ("q_stride", i64), ("workspace_bytes", sz), ("n_seqs", i32), ("max_pages", i32), ("n_q_heads", i32),
+                ("window", i32), ("scale", ctypes.c_float)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     if not os.path.exists(LIB):
@@ -40,12 +53,10 @@ def lib():
     L.w4a4_group_dequantize.argtypes = [ctypes.POINTER(GroupT), vp, vp]
     L.w4a4_group_gemv.argtypes = [vp, i64, ctypes.POINTER(GroupT), vp, vp, u32, vp]
     L.w4a4_rope_table.argtypes = [i32, i32, ctypes.c_double, vp]
-    L.w4a4_kv_append.argtypes = [ctypes.POINTER(CacheT), vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i32, i32, vp,
-                                 vp, vp, i32, i32, vp, u32, vp]
+    L.w4a4_kv_append.argtypes = [ctypes.POINTER(CacheT), ctypes.POINTER(AppendT), vp]
     L.w4a4_kv_attend_workspace_bytes.restype = sz
     L.w4a4_kv_attend_workspace_bytes.argtypes = [i32, i32, i32, i32]
-    L.w4a4_kv_attend.argtypes = [vp, i64, i32, ctypes.POINTER(CacheT), vp, i32, i32, vp, ctypes.c_float, i32, vp, vp,
-                                 vp, sz, vp]
+    L.w4a4_kv_attend.argtypes = [ctypes.POINTER(CacheT), ctypes.POINTER(AttendT), vp]
     return L
 
 
@@ -137,27 +148,30 @@ BAD_CACHES = [(dict(head_dim=96), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED
 
 def test_append_argument_checks(lib):
     def f(cache=None, **kw):
-        a = dict(k=A, ks=256, v=A, vs=256, q=A, qs=512, hq=8, qo=A + 0x1000, T=5, pages=A, n_seqs=5, max_pages=3,
-                 seq=None, pos=A, table=A, n_table=100, rot=64, tpos=None, flags=0)
+        a = dict(k=A, v=A, q=A, q_out=A + 0x1000, k_stride=256, v_stride=256, q_stride=512, n_tokens=5, pages=A,
+                 seq=None, pos=A, table_pos=None, table=A, n_seqs=5, max_pages=3, n_q_heads=8, n_table=100, rot_dim=64,
+                 flags=0)
         a.update(kw)
-        return lib.w4a4_kv_append(cache if cache is not None else _cache(), *a.values(), None)
-    assert f(T=0) == OK and f(T=0, k=None, v=None, q=None, pos=None) == OK
-    assert lib.w4a4_kv_append(None, A, 256, A, 256, A, 512, 8, A, 0, A, 5, 3, None, A, A, 100, 64, None, 0, None) == ARG
+        return lib.w4a4_kv_append(cache if cache is not None else _cache(), ctypes.byref(AppendT(**a)), None)
+    assert f(n_tokens=0) == OK and f(n_tokens=0, k=None, v=None, q=None, pos=None) == OK
+    assert lib.w4a4_kv_append(None, ctypes.byref(AppendT()), None) == ARG
+    assert lib.w4a4_kv_append(_cache(), None, None) == ARG
     for kw, want in BAD_CACHES:
-        assert f(_cache(**kw), T=0) == want, kw
+        assert f(_cache(**kw), n_tokens=0) == want, kw
     for kw in (dict(stride_page=0), dict(stride_token=0), dict(stride_head=0)):
         assert f(_cache(**kw)) == SHAPE
-    for kw in (dict(T=-1), dict(T=1 << 31), dict(n_table=-1), dict(hq=0), dict(n_seqs=-1), dict(max_pages=-1),
+    for kw in (dict(n_tokens=-1), dict(n_tokens=1 << 31), dict(n_table=-1), dict(n_q_heads=0), dict(n_seqs=-1), dict(max_pages=-1),
                dict(n_seqs=(1 << 24) + 1, max_pages=1),
-               dict(n_seqs=1 << 16, max_pages=1 << 15), dict(ks=248), dict(vs=0), dict(qs=504)):
+               dict(n_seqs=1 << 16, max_pages=1 << 15), dict(k_stride=248), dict(v_stride=0), dict(q_stride=504)):
         assert f(**kw) == SHAPE, kw
-    for kw in (dict(k=None), dict(v=None), dict(pos=None), dict(qo=None), dict(table=None), dict(pages=None),
-               dict(qo=A, qs=520)):
+    for kw in (dict(k=None), dict(v=None), dict(pos=None), dict(q_out=None), dict(table=None), dict(pages=None),
+               dict(q_out=A, q_stride=520)):
         assert f(**kw) == ARG, kw
-    for kw in (dict(k=A + 2), dict(v=A + 8), dict(q=A + 4), dict(qo=A + 2), dict(ks=260), dict(vs=257),
-               dict(qs=516), dict(table=A + 4), dict(pos=A + 2), dict(seq=A + 1), dict(tpos=A + 3), dict(pages=A + 2)):
+    for kw in (dict(k=A + 2), dict(v=A + 8), dict(q=A + 4), dict(q_out=A + 2), dict(k_stride=260),
+               dict(v_stride=257), dict(q_stride=516), dict(table=A + 4), dict(pos=A + 2), dict(seq=A + 1),
+               dict(table_pos=A + 3), dict(pages=A + 2)):
         assert f(**kw) == ALIGN, kw
-    for kw in (dict(rot=-16), dict(rot=24), dict(rot=80), dict(flags=0x1)):
+    for kw in (dict(rot_dim=-16), dict(rot_dim=24), dict(rot_dim=80), dict(flags=0x1)):
         assert f(**kw) == UNSUPPORTED, kw
 
 
@@ -168,21 +182,25 @@ def test_attend_argument_checks(lib):
         assert lib.w4a4_kv_attend_workspace_bytes(*args) == 0
 
     def f(cache=None, **kw):
-        a = dict(q=A, qs=512, hq=8, cache=cache if cache is not None else _cache(), pages=A, n_seqs=5, max_pages=3,
-                 lens=A, scale=0.125, window=0, out=A, lse=None, ws=A, wb=need)
+        a = dict(q=A, out=A, lse=None, workspace=A, pages=A, lens=A, q_stride=512, workspace_bytes=need, n_seqs=5,
+                 max_pages=3, n_q_heads=8, window=0, scale=0.125)
         a.update(kw)
-        return lib.w4a4_kv_attend(*a.values(), None)
-    assert f(n_seqs=0) == OK and f(n_seqs=0, q=None, lens=None, out=None, ws=None, wb=0, pages=None) == OK
-    assert lib.w4a4_kv_attend(A, 512, 8, None, A, 5, 3, A, 0.125, 0, A, None, A, need, None) == ARG
+        return lib.w4a4_kv_attend(cache if cache is not None else _cache(), ctypes.byref(AttendT(**a)), None)
+    assert f(n_seqs=0) == OK
+    assert f(n_seqs=0, q=None, lens=None, out=None, workspace=None, workspace_bytes=0, pages=None) == OK
+    assert lib.w4a4_kv_attend(None, ctypes.byref(AttendT()), None) == ARG
+    assert lib.w4a4_kv_attend(_cache(), None, None) == ARG
     for kw, want in BAD_CACHES:
         assert f(_cache(**kw), n_seqs=0) == want, kw
-    for kw in (dict(hq=0), dict(hq=9), dict(hq=1 << 16), dict(window=-1), dict(n_seqs=-1), dict(qs=504),
-               dict(wb=need - 1), dict(cache=_cache(page_size=1 << 29), max_pages=3),
-               dict(cache=_cache(page_size=1 << 28), max_pages=4, n_seqs=32), dict(n_seqs=1 << 16, max_pages=1 << 15, wb=1 << 40)):
+    for kw in (dict(n_q_heads=0), dict(n_q_heads=9), dict(n_q_heads=1 << 16), dict(window=-1), dict(n_seqs=-1),
+               dict(q_stride=504),
+               dict(workspace_bytes=need - 1), dict(cache=_cache(page_size=1 << 29), max_pages=3),
+               dict(cache=_cache(page_size=1 << 28), max_pages=4, n_seqs=32), dict(n_seqs=1 << 16, max_pages=1 << 15, workspace_bytes=1 << 40)):
         assert f(**kw) == SHAPE, kw
-    for kw in (dict(q=None), dict(lens=None), dict(out=None), dict(ws=None), dict(pages=None),
+    for kw in (dict(q=None), dict(lens=None), dict(out=None), dict(workspace=None), dict(pages=None),
                dict(scale=math.nan), dict(scale=math.inf)):
         assert f(**kw) == ARG, kw
-    for kw in (dict(q=A + 2), dict(qs=516), dict(lens=A + 2), dict(out=A + 8), dict(lse=A + 2), dict(ws=A + 4),
+    for kw in (dict(q=A + 2), dict(q_stride=516), dict(lens=A + 2), dict(out=A + 8), dict(lse=A + 2),
+               dict(workspace=A + 4),
                dict(pages=A + 1)):
         assert f(**kw) == ALIGN, kw

@@ -992,64 +992,63 @@ w4a4_status w4a4_rope_table(int32_t n_pos, int32_t rot_dim, double base, float *
   return W4A4_OK;
 }
 
-w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const uint16_t *k, int64_t k_stride, const uint16_t *v,
-                           int64_t v_stride, const uint16_t *q, int64_t q_stride, int32_t n_q_heads,
-                           uint16_t *q_out, int64_t T, const int32_t *pages, int32_t n_seqs, int32_t max_pages,
-                           const int32_t *seq, const int32_t *pos, const float *table, int32_t n_table,
-                           int32_t rot_dim, const int32_t *table_pos, uint32_t flags, void *stream) {
+w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t *tokens, void *stream) {
   using namespace w4a4;
   AppendArgs a = {};
   w4a4_status st = check_cache(cache, &a.cache);
   if (st != W4A4_OK) return st;
-  if (flags & ~W4A4_FLAG_ROPE_PAIRS) return W4A4_ERR_UNSUPPORTED;
-  const int D = cache->head_dim;
-  if (rot_dim < 0 || rot_dim > D || rot_dim % 16) return W4A4_ERR_UNSUPPORTED;
-  if (T < 0 || T >= (int64_t(1) << 31) || n_table < 0 || (q && (n_q_heads < 1 || n_q_heads > 65535)))
+  if (!tokens) return W4A4_ERR_ARG;
+  const w4a4_kv_append_t &t = *tokens;
+  if (t.flags & ~W4A4_FLAG_ROPE_PAIRS) return W4A4_ERR_UNSUPPORTED;
+  const int D = cache->head_dim, Hk = a.cache.heads, Hq = t.q ? t.n_q_heads : 0;
+  if (t.rot_dim < 0 || t.rot_dim > D || t.rot_dim % 16) return W4A4_ERR_UNSUPPORTED;
+  if (t.n_tokens < 0 || t.n_tokens >= (int64_t(1) << 31) || t.n_table < 0 || (t.q && (Hq < 1 || Hq > 65535)))
     return W4A4_ERR_SHAPE;
-  if ((st = check_pages(pages, n_seqs, max_pages)) != W4A4_OK) return st;
+  if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
   if ((a.cache.n_pages > 1 && a.cache.stride_page == 0) || (a.cache.page_size > 1 && a.cache.stride_token == 0) ||
-      (a.cache.heads > 1 && a.cache.stride_head == 0))
+      (Hk > 1 && a.cache.stride_head == 0))
     return W4A4_ERR_SHAPE;
-  if (T == 0) return W4A4_OK;
-  if (!k || !v || !pos || (q && !q_out) || (rot_dim && n_table && !table)) return W4A4_ERR_ARG;
-  if (k_stride < static_cast<int64_t>(a.cache.heads) * D || v_stride < static_cast<int64_t>(a.cache.heads) * D ||
-      (q && q_stride < static_cast<int64_t>(n_q_heads) * D))
+  if (t.n_tokens == 0) return W4A4_OK;
+  if (!t.k || !t.v || !t.pos || (t.q && !t.q_out) || (t.rot_dim && t.n_table && !t.table)) return W4A4_ERR_ARG;
+  if (t.k_stride < static_cast<int64_t>(Hk) * D || t.v_stride < static_cast<int64_t>(Hk) * D ||
+      (t.q && t.q_stride < static_cast<int64_t>(Hq) * D))
     return W4A4_ERR_SHAPE;
-  if (q && q == q_out && q_stride != static_cast<int64_t>(n_q_heads) * D) return W4A4_ERR_ARG;
-  if (!ptr_aligned16(k) || !ptr_aligned16(v) || !ptr_aligned16(q) || (q && !ptr_aligned16(q_out)) ||
-      !ptr_aligned16(table) || !ptr_aligned4(seq) || !ptr_aligned4(pos) || !ptr_aligned4(table_pos) || k_stride % 8 || v_stride % 8 || (q && q_stride % 8))
+  if (t.q && t.q == t.q_out && t.q_stride != static_cast<int64_t>(Hq) * D) return W4A4_ERR_ARG;
+  if (!ptr_aligned16(t.k) || !ptr_aligned16(t.v) || !ptr_aligned16(t.q) || (t.q && !ptr_aligned16(t.q_out)) ||
+      !ptr_aligned16(t.table) || !ptr_aligned4(t.seq) || !ptr_aligned4(t.pos) || !ptr_aligned4(t.table_pos) ||
+      t.k_stride % 8 || t.v_stride % 8 || (t.q && t.q_stride % 8))
     return W4A4_ERR_ALIGN;
-  a.pages = {pages, n_seqs, max_pages};
-  a.k = k;
-  a.v = v;
-  a.q = q;
-  a.q_out = q_out;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  a.q_stride = q_stride;
-  a.q_heads = q ? n_q_heads : 0;
+  a.pages = {t.pages, t.n_seqs, t.max_pages};
+  a.k = t.k;
+  a.v = t.v;
+  a.q = t.q;
+  a.q_out = t.q_out;
+  a.k_stride = t.k_stride;
+  a.v_stride = t.v_stride;
+  a.q_stride = t.q_stride;
+  a.q_heads = Hq;
   a.head_dim = D;
-  a.rot_dim = rot_dim;
-  a.n_table = n_table;
-  a.seq = seq;
-  a.pos = pos;
-  a.table_pos = table_pos;
-  a.table = table;
-  a.pairs = (flags & W4A4_FLAG_ROPE_PAIRS) != 0;
+  a.rot_dim = t.rot_dim;
+  a.n_table = t.n_table;
+  a.seq = t.seq;
+  a.pos = t.pos;
+  a.table_pos = t.table_pos;
+  a.table = t.table;
+  a.pairs = (t.flags & W4A4_FLAG_ROPE_PAIRS) != 0;
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
   cudaLaunchAttribute attr;
   // shares of a token's heads (at most one per 4 passes of a warp) until there
   // are 8 warps per SM
-  const int heads = 2 * a.cache.heads + a.q_heads, round = 4 * (32 / (D / 16)), most = (heads + round - 1) / round;
-  const int64_t want = (8ll * device_sm_count() + T - 1) / T;
+  const int round = 4 * (32 / (D / 16)), most = (2 * Hk + Hq + round - 1) / round;
+  const int64_t want = (8ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
   const int parts = static_cast<int>(want < most ? want : most);
   const cudaLaunchConfig_t cfg =
-      launch_config((T * parts + kAppendWarps - 1) / kAppendWarps, 32 * kAppendWarps, 0, stream, &attr);
+      launch_config((t.n_tokens * parts + kAppendWarps - 1) / kAppendWarps, 32 * kAppendWarps, 0, stream, &attr);
   const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0;
   auto kern = D == 64 ? (fp16 ? kv_append_kernel<Fp16, 64> : kv_append_kernel<Bf16, 64>)
                       : (fp16 ? kv_append_kernel<Fp16, 128> : kv_append_kernel<Bf16, 128>);
-  return launch_status(cudaLaunchKernelEx(&cfg, kern, a, T, parts, status));
+  return launch_status(cudaLaunchKernelEx(&cfg, kern, a, t.n_tokens, parts, status));
 }
 
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
@@ -1058,49 +1057,48 @@ size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t
   return w4a4::part_bytes(n_q_heads / n_kv_heads, head_dim);
 }
 
-w4a4_status w4a4_kv_attend(const uint16_t *q, int64_t q_stride, int32_t n_q_heads, const w4a4_kv_cache_t *cache,
-                           const int32_t *pages, int32_t n_seqs, int32_t max_pages, const int32_t *lens,
-                           float scale, int32_t window, uint16_t *out, float *lse, void *workspace,
-                           size_t workspace_bytes, void *stream) {
+w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t *tokens, void *stream) {
   using namespace w4a4;
   AttendArgs a = {};
   w4a4_status st = check_cache(cache, &a.cache);
   if (st != W4A4_OK) return st;
-  const int D = cache->head_dim;
-  if (n_q_heads < 1 || n_q_heads > 65535 || n_q_heads % a.cache.heads || window < 0) return W4A4_ERR_SHAPE;
-  if ((st = check_pages(pages, n_seqs, max_pages)) != W4A4_OK) return st;
-  if (static_cast<int64_t>(max_pages) * a.cache.page_size > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
-  if (!std::isfinite(scale)) return W4A4_ERR_ARG;
-  if (n_seqs == 0) return W4A4_OK;
-  if (!q || !lens || !out || !workspace) return W4A4_ERR_ARG;
-  if (q_stride < static_cast<int64_t>(n_q_heads) * D) return W4A4_ERR_SHAPE;
-  if (workspace_bytes < w4a4_kv_attend_workspace_bytes(n_seqs, n_q_heads, a.cache.heads, D)) return W4A4_ERR_SHAPE;
-  if (!ptr_aligned16(q) || !ptr_aligned4(lens) || !ptr_aligned16(out) || !ptr_aligned4(lse) ||
-      !ptr_aligned16(workspace) || q_stride % 8)
+  if (!tokens) return W4A4_ERR_ARG;
+  const w4a4_kv_attend_t &t = *tokens;
+  const int D = cache->head_dim, Hk = a.cache.heads, Hq = t.n_q_heads;
+  if (Hq < 1 || Hq > 65535 || Hq % Hk || t.window < 0) return W4A4_ERR_SHAPE;
+  if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
+  if (static_cast<int64_t>(t.max_pages) * a.cache.page_size > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
+  if (!std::isfinite(t.scale)) return W4A4_ERR_ARG;
+  if (t.n_seqs == 0) return W4A4_OK;
+  if (!t.q || !t.lens || !t.out || !t.workspace) return W4A4_ERR_ARG;
+  if (t.q_stride < static_cast<int64_t>(Hq) * D) return W4A4_ERR_SHAPE;
+  if (t.workspace_bytes < w4a4_kv_attend_workspace_bytes(t.n_seqs, Hq, Hk, D)) return W4A4_ERR_SHAPE;
+  if (!ptr_aligned16(t.q) || !ptr_aligned4(t.lens) || !ptr_aligned16(t.out) || !ptr_aligned4(t.lse) ||
+      !ptr_aligned16(t.workspace) || t.q_stride % 8)
     return W4A4_ERR_ALIGN;
-  a.pages = {pages, n_seqs, max_pages};
-  a.q = q;
-  a.q_stride = q_stride;
-  a.q_heads = n_q_heads;
-  a.lens = lens;
-  a.group = n_q_heads / a.cache.heads;
+  a.pages = {t.pages, t.n_seqs, t.max_pages};
+  a.q = t.q;
+  a.q_stride = t.q_stride;
+  a.q_heads = Hq;
+  a.lens = t.lens;
+  a.group = Hq / Hk;
   a.chunks = (a.group + kChunk - 1) / kChunk;
   a.chunk = (a.group + a.chunks - 1) / a.chunks;
-  a.team = a.cache.heads % 4 == 0 ? 4 : a.cache.heads % 2 == 0 ? 2 : 1;
+  a.team = Hk % 4 == 0 ? 4 : Hk % 2 == 0 ? 2 : 1;
   {  // the line of pieces is counted in 32 bits
-    const int64_t pieces = (static_cast<int64_t>(max_pages) * a.cache.page_size + 15) / 16;
-    const int64_t items = static_cast<int64_t>(a.cache.heads / a.team) * a.chunks;
-    if (items * pieces >= (int64_t(1) << 31) / n_seqs) return W4A4_ERR_SHAPE;
+    const int64_t pieces = (static_cast<int64_t>(t.max_pages) * a.cache.page_size + 15) / 16;
+    const int64_t items = static_cast<int64_t>(Hk / a.team) * a.chunks;
+    if (items * pieces >= (int64_t(1) << 31) / t.n_seqs) return W4A4_ERR_SHAPE;
   }
   int shift = 0;  // page_size <= 2^shift
   while ((int64_t(1) << shift) < a.cache.page_size) ++shift;
   a.div_shift = 31 + shift;
   a.div_mul = static_cast<uint32_t>((uint64_t(1) << a.div_shift) / a.cache.page_size + 1);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.window = window;
-  a.out = out;
-  a.lse = lse;
-  a.part = static_cast<float *>(workspace);
+  a.scale_log2 = t.scale * 1.4426950408889634f;
+  a.window = t.window;
+  a.out = t.out;
+  a.lse = t.lse;
+  a.part = static_cast<float *>(t.workspace);
   const bool fp16 = (cache->flags & W4A4_FLAG_FP16) != 0, wide = a.chunk > 8;
   if (D == 64) {
     if (fp16) return wide ? launch_attend<Fp16, 64, 2>(a, stream) : launch_attend<Fp16, 64, 1>(a, stream);

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -105,13 +106,13 @@ _group_dequantize = _sig("w4a4_group_dequantize", ctypes.c_int, [ctypes.POINTER(
 _group_gemv = _sig("w4a4_group_gemv", ctypes.c_int,
                    [_vp, _i64, ctypes.POINTER(GroupWeightsT), _vp, _vp, _u32, _vp])
 _rope_table = _sig("w4a4_rope_table", ctypes.c_int, [_i32, _i32, ctypes.c_double, _vp])
-_kv_append = _sig("w4a4_kv_append", ctypes.c_int,
-                  [ctypes.POINTER(KVCacheT), _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp, _i32, _i32,
-                   _vp, _vp, _vp, _i32, _i32, _vp, _u32, _vp])
+_kv_append = _sig("w4a4_kv_append", ctypes.c_int, [ctypes.POINTER(KVCacheT), ctypes.c_char_p, _vp])
 _kv_attend_ws = _sig("w4a4_kv_attend_workspace_bytes", _sz, [_i32, _i32, _i32, _i32])
-_kv_attend = _sig("w4a4_kv_attend", ctypes.c_int,
-                  [_vp, _i64, _i32, ctypes.POINTER(KVCacheT), _vp, _i32, _i32, _vp, _f32, _i32, _vp, _vp, _vp,
-                   _sz, _vp])
+_kv_attend = _sig("w4a4_kv_attend", ctypes.c_int, [ctypes.POINTER(KVCacheT), ctypes.c_char_p, _vp])
+# w4a4_kv_append_t and w4a4_kv_attend_t, field by field (packing them costs a third of what
+# ctypes takes to convert as many arguments)
+_append_t = struct.Struct("PPPPqqqqPPPPPiiiiiI")
+_attend_t = struct.Struct("PPPPPPqNiiiif4x")
 _status_string = _sig("w4a4_status_string", ctypes.c_char_p, [ctypes.c_int])
 _version = _sig("w4a4_version", ctypes.c_char_p, [])
 
@@ -600,8 +601,7 @@ def w4a4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pages: torc
     T = k.shape[0]
     kp, ks = _rows(k, "k", dt, dev, (T, cache.n_heads, cache.head_dim))
     vp, vs = _rows(v, "v", dt, dev, (T, cache.n_heads, cache.head_dim))
-    qp = op = tp = None
-    qs = hq = n_table = rot = 0
+    qp = qs = op = hq = tp = n_table = rot = 0
     if q is not None:
         hq = q.shape[1]
         shape = (T, hq, cache.head_dim)
@@ -617,12 +617,11 @@ def w4a4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, pages: torc
         tp = _need(table, "table", torch.float32, dev, (n_table, rot))
     if seq is None and T > n_seqs:
         raise ValueError(f"{T} tokens for {n_seqs} sequences need seq")
-    _check(_kv_append(cache.ref, kp, ks, vp, vs, qp, qs, hq, op, T,
-                      _need(pages, "pages", torch.int32, dev, (n_seqs, max_pages)), n_seqs, max_pages,
-                      None if seq is None else _need(seq, "seq", torch.int32, dev, (T,)),
-                      _need(pos, "pos", torch.int32, dev, (T,)), tp, n_table, rot,
-                      None if table_pos is None else _need(table_pos, "table_pos", torch.int32, dev, (T,)),
-                      flags, st), "w4a4_kv_append")
+    _check(_kv_append(cache.ref, _append_t.pack(
+        kp, vp, qp, op, ks, vs, qs, T, _need(pages, "pages", torch.int32, dev, (n_seqs, max_pages)),
+        0 if seq is None else _need(seq, "seq", torch.int32, dev, (T,)), _need(pos, "pos", torch.int32, dev, (T,)),
+        0 if table_pos is None else _need(table_pos, "table_pos", torch.int32, dev, (T,)), tp,
+        n_seqs, max_pages, hq, n_table, rot, flags), st), "w4a4_kv_append")
     return None if q is None else q_out
 
 
@@ -644,7 +643,7 @@ def w4a4_kv_attend(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: t
     qp, qs = _rows(q, "q", dt, dev, (B, Hq, cache.head_dim))
     max_pages = pages.shape[1]
     if out is None:
-        out = q.new_empty((B, Hq, D))
+        out = torch.empty_like(q) if q.is_contiguous() else q.new_empty((B, Hq, D))
         op = out.data_ptr()
     else:
         op = _need(out, "out", dt, dev, (B, Hq, D))
@@ -653,8 +652,9 @@ def w4a4_kv_attend(q: torch.Tensor, cache: KVCache, pages: torch.Tensor, lens: t
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace: need a contiguous tensor on {dev}")
-    _check(_kv_attend(qp, qs, Hq, cache.ref, _need(pages, "pages", torch.int32, dev, (B, max_pages)), B, max_pages,
-                      _need(lens, "lens", torch.int32, dev, (B,)), D ** -0.5 if scale is None else scale, window, op,
-                      None if lse is None else _need(lse, "lse", torch.float32, dev, (B, Hq)),
-                      workspace.data_ptr(), workspace.nbytes, st), "w4a4_kv_attend")
+    _check(_kv_attend(cache.ref, _attend_t.pack(
+        qp, op, 0 if lse is None else _need(lse, "lse", torch.float32, dev, (B, Hq)), workspace.data_ptr(),
+        _need(pages, "pages", torch.int32, dev, (B, max_pages)), _need(lens, "lens", torch.int32, dev, (B,)),
+        qs, workspace.nbytes, B, max_pages, Hq, window, D ** -0.5 if scale is None else scale), st),
+        "w4a4_kv_attend")
     return out
