@@ -913,15 +913,14 @@ w4a4_status check_pages(const int32_t *pages, int32_t n_seqs, int32_t max_pages)
   return ptr_aligned4(pages) ? W4A4_OK : W4A4_ERR_ALIGN;
 }
 
-cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr,
-                                 bool early = true) {
+cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr->val.programmaticStreamSerializationAllowed = early;
+  attr->val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cfg;
@@ -959,11 +958,7 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   if (grid < 1) grid = 1;
   const int teams = static_cast<int>(grid) * teams_here;
   cudaLaunchAttribute attr;
-  // Where every place is needed, not before the kernel in front is done: blocks that
-  // wait beside the join of the call before keep others from finding one at once (64
-  // sequences of 8k: 155 us in a row of calls, 129 without).
-  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr,
-                                         2 * grid <= static_cast<int64_t>(device_sm_count()) * per_sm);
+  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
   // one team, or items of one piece: nothing is shared
   if (e != cudaSuccess || teams == 1 || pieces <= 1) return launch_status(e);
