@@ -85,8 +85,8 @@ template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
     group_quantize_kernel(const uint16_t *__restrict__ W, GroupShape s, uint8_t *__restrict__ data) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;  // groups of a block, words j of a group
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31;
@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 __global__ void __launch_bounds__(32 * kPackWarps)
     group_pack_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, GroupShape s,
                       uint8_t *__restrict__ data) {
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31, per = kBlockK / s.group;
@@ -188,8 +188,8 @@ template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
     group_dequantize_kernel(const uint8_t *__restrict__ data, GroupShape s, uint16_t *__restrict__ W) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;
-  griddep_launch_dependents();
   griddep_wait();
+  griddep_launch_dependents();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31;
@@ -319,7 +319,6 @@ __global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(
     }
   };
 
-  griddep_launch_dependents();
   for (int set = blockIdx.x; set < a.sets; set += gridDim.x) {
     const int tile0 = static_cast<int>(static_cast<int64_t>(set) * s.tiles / a.sets);
     const int tiles = static_cast<int>(static_cast<int64_t>(set + 1) * s.tiles / a.sets) - tile0;
@@ -351,6 +350,7 @@ __global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(
       }
       from = from0, copy_u = units - u0;
       griddep_wait();
+      griddep_launch_dependents();
     }
     auto fill = [&]() {
       if (--copies >= 0) {
