@@ -249,7 +249,7 @@ constexpr int gemv_warps(int RT, int NT) { return RT * NT > 16 ? 8 : 16; }
 // Tiles that a warp takes in one go: two, whose products do not depend on one another and
 // which share the waiting and counting, unless there is only one.
 constexpr int gemv_pair(int RT) { return RT > 1 ? 2 : 1; }
-constexpr int gemv_stages(int RT, int NT) { return 128 / gemv_warps(RT, NT) / gemv_pair(RT); }
+constexpr int gemv_stages(int RT, int NT) { return 64 / gemv_warps(RT, NT) / gemv_pair(RT); }
 
 struct GemvArgs {
   const uint16_t *X;
@@ -532,7 +532,7 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kGemvWarps = gemv_warps(RT, NT), kRing = 128 * record_bytes(GROUP);
+  constexpr int kGemvWarps = gemv_warps(RT, NT), kRing = 64 * record_bytes(GROUP);
   constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
   static ContextCache<int> ready;  // per context: attribute set
   int done = 0;
@@ -553,7 +553,8 @@ w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
   const int tiles = (a.s.tiles - 1) / device_sm_count() + 1;
   if (a.M <= 8) {
     if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 1>(a, stream);
-    return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 1>(a, stream) : launch_gemv_t<T, GROUP, 16, 1>(a, stream);
+    if (tiles <= 4) return launch_gemv_t<T, GROUP, 4, 1>(a, stream);
+    return tiles <= 8 ? launch_gemv_t<T, GROUP, 8, 1>(a, stream) : launch_gemv_t<T, GROUP, 16, 1>(a, stream);
   }
   if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 2>(a, stream);
   return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 2>(a, stream) : launch_gemv_t<T, GROUP, 16, 2>(a, stream);
