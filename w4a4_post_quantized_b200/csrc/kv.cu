@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //    most: its first and its last), and kv_join_kernel joins those.
 //  * A warp works alone, through its own ring of stages filled by 16-byte asynchronous
 //    copies that run ahead across the ends of items: no block-wide wait anywhere.
-//    Where pages hold a multiple of a piece, a piece is one page's; otherwise rows
-//    are looked up one by one.  Rows without a token are filled with zeros by the copy
+//    A piece that lies in one page is looked up once, one that does not row by row.  Rows without a token are filled with zeros by the copy
 //    itself.
 //  * The products are m16n8k16 tensor-core instructions (a piece has at most 16
 //    rows of queries, so tcgen05's 128-row tiles would be nearly empty, and at
@@ -222,7 +221,6 @@ struct AttendArgs {
   int q_heads, group;                // query heads, and how many share a cache head
   int chunks, chunk;                 // chunks of a group, heads of a chunk
   int team;                          // warps (cache heads) of a team: 4, 2 or 1
-  bool whole;                        // pages hold a multiple of a piece's tokens
   uint32_t div_mul;                  // t / page_size = (t * div_mul) >> div_shift, t < 2^31
   int div_shift;
   const int32_t *lens;
@@ -412,9 +410,9 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   Range<P> range = cr;
   const int64_t values = a.cache.v - a.cache.k;
   const int crow = lane / kPieces, cpos = lane % kPieces;
-  bool absent = false, ready = false;
-  // the piece that is looked up: of its first token (whole) or token lane % P, the page, and
-  // the place without the page's; a page is not used before the copies, a round later
+  bool absent = false, ready = false, one = false;
+  // the piece that is looked up: of its first token, where one page holds all of it, or of
+  // token lane % P the page, and the place without the page's; a page is not used before the copies, a round later
   int look_t0 = 0, look_lo = 0, look_hi = 0, page = -1;  // tokens look_t0 + look_lo .. look_hi - 1 are there
   int64_t rest = 0;
   auto look_up = [&]() {
@@ -429,10 +427,15 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
       }
     }
     look_t0 = (cr.p0 + cpiece) * P;
-    const int t = a.whole ? look_t0 : look_t0 + lane % P;
-    const int entry = static_cast<int>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
+    int t = look_t0;
+    int entry = static_cast<int>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
+    one = t - entry * a.cache.page_size + P <= a.cache.page_size;
+    if (!one) {
+      t += lane % P;
+      entry = static_cast<int>((static_cast<uint64_t>(t) * a.div_mul) >> a.div_shift);
+    }
     page = -1;
-    if (a.whole || (t >= cr.first && t < cr.end))
+    if (one || (t >= cr.first && t < cr.end))
       page = __ldg(a.pages.table + static_cast<int64_t>(cb) * a.pages.max_pages + entry);
     rest = static_cast<int64_t>(a.heads_of(citem) * a.team + member) * a.cache.stride_head +
            (t - entry * a.cache.page_size) * a.cache.stride_token;
@@ -449,7 +452,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
       const bool ok = page >= 0 && page < a.cache.n_pages;
       const int64_t row = rest + page * a.cache.stride_page;
       uint32_t live = (kAll >> (P - look_hi)) & (kAll << look_lo);
-      if (a.whole) {
+      if (one) {
         if (!ok) absent = true, live = 0;
       } else {
         const uint32_t found = __ballot_sync(0xffffffffu, ok);
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
         live &= found;
       }
       if (lane == 0) live_rows[warp][stage] = live;
-      if (a.whole && live == kAll) {
+      if (one && live == kAll) {
         const uint16_t *k = a.cache.k + row + crow * a.cache.stride_token + 8 * cpos;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
@@ -471,7 +474,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
           const int rr = i * kRowsPer + crow;
-          const int64_t of = a.whole ? row + rr * a.cache.stride_token : __shfl_sync(0xffffffffu, row, rr);
+          const int64_t of = one ? row + rr * a.cache.stride_token : __shfl_sync(0xffffffffu, row, rr);
           const bool there = (live >> rr) & 1u;
           const uint16_t *k = a.cache.k + of + 8 * cpos;
           const uint32_t to = dst + rr * kRow + swizzle(rr, cpos) * 16;
@@ -946,7 +949,6 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
     return W4A4_ERR_CUDA;
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
-  a.whole = a.cache.page_size % P == 0;
   // blocks: one per place on the GPU, fewer when there cannot be that many pieces
   const int teams_here = kAttendWarps / a.team;
   int64_t grid = static_cast<int64_t>(device_sm_count()) * per_sm;
