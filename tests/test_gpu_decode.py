@@ -483,6 +483,20 @@ def test_attend_large_scores(w4):
     check_attend(w4, q, cache, K, V, pages, lens, scale=0.0)
 
 
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("D,Hq", [(64, 1), (128, 12)])
+def test_attend_many_weights_far_below_the_largest(w4, D, Hq, dt):
+    """One token of score 18 holds value 0, 200000 of score 0 hold 1: weights of 2^-26 that are 2^-8 of
+    the sum together, and all of the result."""
+    n, page = 200_000, 64
+    K, V = torch.zeros(n // page, page, 1, D, dtype=dt), torch.ones(n // page, page, 1, D, dtype=dt)
+    K[1000, 7, 0, 0], V[1000, 7] = 4.5, 0.0
+    q = torch.zeros(1, Hq, D, dtype=dt)
+    q[..., 0] = 4.0
+    pages = torch.arange(n // page, dtype=torch.int32).view(1, -1)
+    check_attend(w4, q, w4.KVCache(K.cuda(), V.cuda()), K, V, pages, torch.tensor([n], dtype=torch.int32), scale=1.0)
+
+
 def test_attend_lowest_scores(w4):
     """All scores are huge and negative: the softmax still sums to one."""
     q, cache, K, V, pages, lens = attend_case(w4, 2, [50, 1], 2, 1, 64, 16, "nhd", BF16, 13)

@@ -21,6 +21,8 @@ __device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) 
 }
 
 struct Bf16 {
+  // log2 of the largest softmax weight: the type's range is that of fp32
+  static constexpr float kTop = 0.0f;
   static __device__ __forceinline__ float to_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
   // element 0 of a packed pair in the low half
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -69,6 +71,9 @@ struct Bf16 {
 };
 
 struct Fp16 {
+  // Weights go up to 2^15, so that those down to 2^-39 of the largest are held (2^-24 is the least there is;
+  // 2^-26 of 1 would be lost, and a hundred thousand of those are 2^-9 of the sum).
+  static constexpr float kTop = 15.0f;
   static __device__ __forceinline__ float to_f32(uint16_t v) { return __half2float(__ushort_as_half(v)); }
   static __device__ __forceinline__ float lo(uint32_t w) { return to_f32(static_cast<uint16_t>(w & 0xFFFFu)); }
   static __device__ __forceinline__ float hi(uint32_t w) { return to_f32(static_cast<uint16_t>(w >> 16)); }

@@ -202,7 +202,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //    so a lane's operands are 16-byte pieces of rows as they lie in memory.
 //  * Weights enter the second product as two 16-bit terms (hi + lo, 2^-16 or
 //    better): one term would put an error of half a bf16 step on every weight,
-//    as large as the rounding of the result.
+//    as large as the rounding of the result.  The reference that is
+//    subtracted from the scores lies kTop below their maximum, so that in fp16 the
+//    small ones are not lost.
 
 constexpr int kAttendWarps = 4;
 constexpr int kMaxBlocks = 448;      // partial results in the workspace: two per warp
@@ -298,7 +300,7 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// The logarithm of a sum of 2^x held as top and sum of 2^(x - top).
+// The logarithm of a sum of 2^x held as top and sum of 2^(x - top); top is any finite reference.
 __device__ __forceinline__ float log_sum(float top, float sum) {
   return sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.69314718055994531f;
 }
@@ -572,7 +574,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
         for (int e = 1; e < P / 4; ++e) top = fmaxf(top, x[e]);
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m[n], top);
+        const float mn = fmaxf(m[n], top - T::kTop);
         const float base = mn == -INFINITY ? 0.0f : mn;
         if (__any_sync(0xffffffffu, mn != m[n])) {
           const float keep = exp2f(m[n] - base);
