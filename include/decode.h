@@ -94,7 +94,8 @@ w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, vo
  * for M <= W4A4_GEMV_MAX_TOKENS tokens (W4A4_ERR_SHAPE above) X [M, K]; bias [N]
  * 16-bit or NULL.  Products of codes and activations are exact, sums are fp32:
  * per group first, then times the step.  flags: 0, or W4A4_FLAG_GELU_OUT (bf16
- * only): Y = bf16(GELU(y)) of the rounded y, as in w4a4_linear_ex. */
+ * only): Y = bf16(GELU(y)) of the rounded y, as in w4a4_linear_ex.  Y must not
+ * overlap X (W4A4_ERR_ARG). */
 w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weights_t *w, const uint16_t *bias,
                             uint16_t *Y, uint32_t flags, void *stream);
 
@@ -143,7 +144,7 @@ typedef struct {
 /* New tokens enter the cache: token t with keys k[t] and values v[t] becomes position pos[t]
  * of sequence seq[t], which lives in page pages[seq, pos / page_size] at row pos %
  * page_size.  Keys, and queries on their way from q to q_out (which may be q itself when
- * q_stride = n_q_heads * head_dim, and must not overlap it otherwise), are rotated: with
+ * q_stride = n_q_heads * head_dim, and must not overlap it otherwise: W4A4_ERR_ARG), are rotated: with
  * (a, b) elements i and i + rot_dim / 2 (W4A4_FLAG_ROPE_PAIRS: 2i and 2i + 1) of a head and
  * (c, s) elements i and i + rot_dim / 2 of the token's row of the table, a' = a c - b s, b' =
  * b c + a s in fp32, rounded once; elements from rot_dim on, values, and everything when
@@ -180,11 +181,15 @@ typedef struct {
  * head h, which reads cache head h / (n_q_heads / n_heads),
  *   out[b, h] = sum_t p_t V[t],  p = softmax_t(scale * q[b, h] . K[t])
  * over positions t in [max(0, lens[b] - window), lens[b]) (window 0: all).
- * Statistics and sums are fp32; the result is rounded once.  A sequence
+ * Statistics and sums are fp32, weights two 16-bit terms (2^-16); the result is rounded once.  A sequence
  * with nothing to attend to (length 0 or negative), or all of whose scores are -inf, gets
  * zeros, and lse = -inf.
- *   - Rows of a page at or behind the length are never used, whatever they
- *     hold.  Pages may be shared between sequences.
+ *   - Rows of a page at or behind the length, or in front of the window, are never used,
+ *     whatever they hold, nor are the pages that hold only such rows.  Pages may be shared
+ *     between sequences.  An infinite value of a token that is attended to gives an infinity
+ *     or NaN in its dimension (of the heads that share it); keys follow the formula.
+ *   - out may be q itself when q_stride = n_q_heads * head_dim, and must not overlap it
+ *     otherwise (W4A4_ERR_ARG).
  *   - max_pages * page_size is at most 2^30, n_seqs at most 2^24, and n_seqs * n_q_heads *
  *     max_pages * page_size / 16 below 2^31 at the least (W4A4_ERR_SHAPE above).
  *   - A length above max_pages * page_size counts as that many, and a row whose

@@ -204,3 +204,30 @@ def test_attend_argument_checks(lib):
                dict(workspace=A + 4),
                dict(pages=A + 1)):
         assert f(**kw) == ALIGN, kw
+
+
+def test_outputs_that_overlap_their_inputs_are_refused(lib):
+    """Every byte offset of an output around its input that matters, against sets of addresses."""
+    G = lib.w4a4_group_gemv
+    assert G(A, 2, _group(), None, A, 0, None) == ARG
+    assert G(A, 2, _group(), None, A + 2 * 2 * 512 - 16, 0, None) == ARG
+    assert G(A, 2, _group(), None, A - 2 * 2 * 256 + 16, 0, None) == ARG
+
+    def append(**kw):
+        a = dict(k=A, v=A, q=A, q_out=A, k_stride=256, v_stride=256, n_tokens=3, pages=A, pos=A, n_seqs=5, max_pages=3,
+                 n_q_heads=2)
+        a.update(kw)
+        return lib.w4a4_kv_append(_cache(), ctypes.byref(AppendT(**a)), None)
+
+    def attend(**kw):
+        a = dict(q=A, out=A, workspace=A, pages=A, lens=A, workspace_bytes=1 << 40, n_seqs=3, max_pages=3, n_q_heads=4,
+                 scale=0.125)
+        a.update(kw)
+        return lib.w4a4_kv_attend(_cache(), ctypes.byref(AttendT(**a)), None)
+    for f, name, width in ((append, "q_out", 2 * 64), (attend, "out", 4 * 64)):
+        for stride in (width, width + 8, 5 * width):
+            used = {t * stride + i for t in range(3) for i in range(width)}
+            for at in range(-3 * width, 3 * stride, 8):
+                if used & set(range(at, at + 3 * width)) and (at, stride) != (0, width):
+                    assert f(**{"q_stride": stride, name: A + 2 * at}) == ARG, (stride, at)
+    assert attend(scale=3e38) == ARG

@@ -497,6 +497,50 @@ def test_attend_many_weights_far_below_the_largest(w4, D, Hq, dt):
     check_attend(w4, q, w4.KVCache(K.cuda(), V.cuda()), K, V, pages, torch.tensor([n], dtype=torch.int32), scale=1.0)
 
 
+def test_attend_in_place_and_into_the_gaps_of_q(w4):
+    """out may be q itself, long sequences split over many warps included, or lie between its rows."""
+    q, cache, K, V, pages, lens = attend_case(w4, 4, [5000, 1, 0, 333], 20, 1, 64, 16, "nhd", BF16, 23)
+    want = w4.w4a4_kv_attend(q.cuda(), cache, pages.cuda(), lens.cuda())
+    qd = q.cuda()
+    assert w4.w4a4_kv_attend(qd, cache, pages.cuda(), lens.cuda(), out=qd) is qd
+    assert torch.equal(qd, want)
+    wide = torch.zeros(4, 5 * 20 * 64, dtype=BF16, device="cuda")
+    wide[:, :20 * 64] = q.view(4, -1).cuda()
+    out = wide[1, 20 * 64:].view(4, 20, 64)
+    w4.w4a4_kv_attend(wide[:, :20 * 64].view(4, 20, 64), cache, pages.cuda(), lens.cuda(), out=out)
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("page", [7, 16, 64])
+def test_attend_window_over_freed_pages(w4, page):
+    """Pages that lie wholly in front of the window need not be there."""
+    q, cache, K, V, pages, lens = attend_case(w4, 3, [500, 321, 90], 4, 2, 64, page, "nhd", BF16, 24)
+    want = w4.w4a4_kv_attend(q.cuda(), cache, pages.cuda(), lens.cuda(), window=75)
+    freed = pages.clone()
+    for b, n in enumerate(lens.tolist()):
+        freed[b, :(n - 75) // page] = 1 << 30
+    got = w4.w4a4_kv_attend(q.cuda(), cache, freed.cuda(), lens.cuda(), window=75)
+    assert torch.equal(got, want)                  # and the status stays clear
+
+
+@pytest.mark.parametrize("page", [1, 7, 24])
+def test_attend_absent_pages_that_end_inside_a_tile(w4, page):
+    """Pages out of range among rows that are looked up one by one: left out and reported."""
+    n, D = 200, 128
+    q, cache, K, V, pages, lens = attend_case(w4, 1, [n], 4, 2, D, page, "nhd", FP16, 25)
+    bad = pages.clone()
+    gone = [0, 3, (n - 1) // page]
+    bad[0, gone] = torch.tensor([-1, 1 << 30, cache.n_pages], dtype=torch.int32)
+    out = w4.w4a4_kv_attend(q.cuda(), cache, bad.cuda(), lens.cuda())
+    assert w4.w4a4_get_device_status() == RANGE
+    w4.w4a4_clear_device_status()
+    keep = torch.tensor([t for t in range(n) if t // page not in gone])
+    row = pages[0, keep // page].long(), keep % page
+    want, _, bound, _ = oracle_attend(q, K[row][:, None], V[row][:, None], torch.arange(len(keep)).view(1, -1),
+                                      torch.tensor([len(keep)]), D ** -0.5, 0)
+    close(out, want, bound, FP16)
+
+
 def test_attend_lowest_scores(w4):
     """All scores are huge and negative: the softmax still sums to one."""
     q, cache, K, V, pages, lens = attend_case(w4, 2, [50, 1], 2, 1, 64, 16, "nhd", BF16, 13)
@@ -673,6 +717,51 @@ def test_a_step_captured_and_replayed(w4):
         assert torch.equal(outs[t % 2], want[t]), t
 
 
+def test_graphs_that_share_a_workspace(w4):
+    """Two captured calls of different shapes over one workspace, and an eager one between them."""
+    cases = [attend_case(w4, 2, [9000, 4000], 8, 4, 64, 16, "nhd", BF16, 81),
+             attend_case(w4, 3, [100, 7000, 3], 16, 1, 128, 64, "hnd", BF16, 82)]
+    args = [(c[0].cuda(), c[1], c[4].cuda(), c[5].cuda()) for c in cases]
+    want = [w4.w4a4_kv_attend(*a) for a in args]
+    need = max(w4.w4a4_kv_attend_workspace_bytes(a[0].shape[0], a[0].shape[1], a[1].n_heads, a[0].shape[2])
+               for a in args)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for a in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(w4.w4a4_kv_attend(*a, workspace=ws))
+        graphs.append(g)
+    for _ in range(5):
+        for o in outs:
+            o.fill_(7.0)
+        graphs[0].replay()
+        eager = w4.w4a4_kv_attend(*args[1], workspace=ws)
+        graphs[1].replay()
+        graphs[0].replay()
+        assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1]) and torch.equal(eager, want[1])
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_a_padded_batch(w4, dt):
+    """Rows without a sequence (position -1, length 0, tokens of NaN) change nothing of the others, and
+    leave the attention's zeros behind."""
+    S, Hq, H, D = 5, 4, 2, 64
+    full, padded = (Block(w4, S, Hq, H, D, 64, dt, 91) for _ in range(2))
+    x = torch.randn(S, Hq * D, generator=gen(92)).to(dt).cuda()
+    pos = torch.zeros(S, dtype=torch.int32, device="cuda")
+    want = full.step(x, pos, pos + 1)
+    x, pos = x.clone(), pos.clone()
+    x[1], x[4], pos[1], pos[4] = math.nan, math.inf, -1, -1
+    got = padded.step(x, pos, pos + 1)             # one token each, so no item is split differently
+    live = [0, 2, 3]
+    assert torch.equal(got[live], want[live]) and torch.all(got[[1, 4]] == 0)
+    for a, b in ((full.cache.k, padded.cache.k), (full.cache.v, padded.cache.v)):
+        rows = full.pages_d[live, 0].long()
+        assert torch.equal(a[rows, 0], b[rows, 0])
+        assert b.isnan().flatten(1).any(1).all() and b[padded.pages_d[[1, 4], 0].long()].isnan().all()
+
+
 def test_first_calls_in_a_capture():
     """The first use of every operator in a process may be a captured one."""
     code = (
@@ -749,6 +838,9 @@ def test_refusals_of_the_binding(w4):
         w4.w4a4_group_gemv(x, w, bias=torch.zeros(15, dtype=BF16, device=dev))
     with pytest.raises(ValueError):
         w4.w4a4_group_gemv(x, w, Y=torch.zeros(2, 17, dtype=BF16, device=dev))
+    square = w4.w4a4_group_quantize(torch.zeros(128, 128, dtype=BF16, device=dev))
+    with pytest.raises(w4.W4A4Error):
+        w4.w4a4_group_gemv(x, square, Y=x)
     with pytest.raises(w4.W4A4Error):
         w4.w4a4_group_gemv(torch.zeros(17, 128, dtype=BF16, device=dev), w)
     with pytest.raises(w4.W4A4Error):

@@ -124,6 +124,13 @@ struct Fp16 {
 
 inline bool ptr_aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline bool ptr_aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+// Whether any of `rows` runs of `row` elements, `stride` apart from a on, shares memory with the n elements at b.
+inline bool overlap(const uint16_t *a, int64_t rows, int64_t row, int64_t stride, const uint16_t *b, int64_t n) {
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a)) / 2;
+  // the first run that ends behind b
+  const int64_t t = at < row || stride == 0 ? 0 : (at - row) / stride + 1;
+  return t < rows && t * stride + row > at && t * stride < at + n;
+}
 inline w4a4_status launch_status(cudaError_t e) { return e == cudaSuccess ? W4A4_OK : W4A4_ERR_CUDA; }
 
 }  // namespace

@@ -629,6 +629,7 @@ w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weigh
   if (M == 0) return W4A4_OK;
   if (!X || !Y) return W4A4_ERR_ARG;
   if (!ptr_aligned16(X) || !ptr_aligned16(Y) || (bias && !ptr_aligned16(bias))) return W4A4_ERR_ALIGN;
+  if (overlap(X, 1, M * w->K, 0, Y, M * w->N)) return W4A4_ERR_ARG;
   const GemvArgs a{X, static_cast<int>(M), w->data, shape_of(w->N, w->K, w->group), bias, Y, gelu, 0};
   switch (w->group) {
     case 32: return fp16 ? launch_gemv<Fp16, 32>(a, stream) : launch_gemv<Bf16, 32>(a, stream);

@@ -209,6 +209,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 constexpr int kAttendWarps = 4;
 constexpr int kMaxBlocks = 448;      // partial results in the workspace: two per warp
 constexpr int kChunk = 16;           // most query heads of a warp's item
+constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int attend_piece(int D) { return D == 64 ? 32 : 16; }  // tokens of a stage: 8 KB of keys and values
 // Stages of a warp's ring: with two, three blocks fit on an SM.  (Two blocks with three
@@ -918,6 +919,11 @@ w4a4_status check_pages(const int32_t *pages, int32_t n_seqs, int32_t max_pages)
   return ptr_aligned4(pages) ? W4A4_OK : W4A4_ERR_ALIGN;
 }
 
+// Whether the output takes part of the queries' memory, other than all of it in place.
+bool out_in_q(const uint16_t *q, int64_t stride, int64_t rows, int64_t row, const uint16_t *out) {
+  return !(q == out && (rows == 1 || stride == row)) && overlap(q, rows, row, stride, out, rows * row);
+}
+
 cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
@@ -1012,11 +1018,11 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   if (t.k_stride < static_cast<int64_t>(Hk) * D || t.v_stride < static_cast<int64_t>(Hk) * D ||
       (t.q && t.q_stride < static_cast<int64_t>(Hq) * D))
     return W4A4_ERR_SHAPE;
-  if (t.q && t.q == t.q_out && t.q_stride != static_cast<int64_t>(Hq) * D) return W4A4_ERR_ARG;
   if (!ptr_aligned16(t.k) || !ptr_aligned16(t.v) || !ptr_aligned16(t.q) || (t.q && !ptr_aligned16(t.q_out)) ||
       !ptr_aligned16(t.table) || !ptr_aligned4(t.seq) || !ptr_aligned4(t.pos) || !ptr_aligned4(t.table_pos) ||
       t.k_stride % 8 || t.v_stride % 8 || (t.q && t.q_stride % 8))
     return W4A4_ERR_ALIGN;
+  if (t.q && out_in_q(t.q, t.q_stride, t.n_tokens, static_cast<int64_t>(Hq) * D, t.q_out)) return W4A4_ERR_ARG;
   a.pages = {t.pages, t.n_seqs, t.max_pages};
   a.k = t.k;
   a.v = t.v;
@@ -1067,7 +1073,7 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   if (Hq < 1 || Hq > 65535 || Hq % Hk || t.window < 0) return W4A4_ERR_SHAPE;
   if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
   if (static_cast<int64_t>(t.max_pages) * a.cache.page_size > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
-  if (!std::isfinite(t.scale)) return W4A4_ERR_ARG;
+  if (!std::isfinite(t.scale * kLog2e)) return W4A4_ERR_ARG;
   if (t.n_seqs == 0) return W4A4_OK;
   if (!t.q || !t.lens || !t.out || !t.workspace) return W4A4_ERR_ARG;
   if (t.q_stride < static_cast<int64_t>(Hq) * D) return W4A4_ERR_SHAPE;
@@ -1075,6 +1081,7 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   if (!ptr_aligned16(t.q) || !ptr_aligned4(t.lens) || !ptr_aligned16(t.out) || !ptr_aligned4(t.lse) ||
       !ptr_aligned16(t.workspace) || t.q_stride % 8)
     return W4A4_ERR_ALIGN;
+  if (out_in_q(t.q, t.q_stride, t.n_seqs, static_cast<int64_t>(Hq) * D, t.out)) return W4A4_ERR_ARG;
   a.pages = {t.pages, t.n_seqs, t.max_pages};
   a.q = t.q;
   a.q_stride = t.q_stride;
@@ -1093,7 +1100,7 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   while ((int64_t(1) << shift) < a.cache.page_size) ++shift;
   a.div_shift = 31 + shift;
   a.div_mul = static_cast<uint32_t>((uint64_t(1) << a.div_shift) / a.cache.page_size + 1);
-  a.scale_log2 = t.scale * 1.4426950408889634f;
+  a.scale_log2 = t.scale * kLog2e;
   a.window = t.window;
   a.out = t.out;
   a.lse = t.lse;
