@@ -38,7 +38,7 @@ __device__ __forceinline__ int nibble_shift(int e) { return 4 * ((e >> 1) + 4 * 
 // warp's 512 in a row), a group's maximum needs two exchanges between four
 // lanes, and all eight 16-byte loads are in flight at once.  (One thread per 8
 // inputs, with the rows' order on both sides: 20000 x 8192 there and back took 411
-// us.)
+// us; now 65 and 64, 99 % of a copy's rate.)
 
 constexpr int kPackWarps = 8;
 
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    subtraction the exact codes.
 //  * A group's products are summed in fp32 by the tensor core, multiplied by the
 //    step and added to the fp32 total: the codes stay exact and no weight is rounded.
-//  * One block of 16 warps per SM takes an equal share of the 16-row tiles, up to RT at a
-//    time, and keeps their sums in registers.  The line (block of 128 inputs, tile)
+//  * One block of 16 warps (8, for large shapes and more than 8 tokens) per SM takes an equal
+//    share of the 16-row tiles, up to RT at a time, and keeps their sums in registers.  The line (block of 128 inputs, tile)
 //    is cut evenly between the warps: a warp reads a block's tokens once and uses them for
 //    all the tiles, while codes and steps stream through its own ring of
 //    asynchronous copies.  At the end the warps' sums meet in shared memory, where the rings
@@ -241,15 +241,26 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    tokens that L1 could not hold.)
 //  * Before it waits for the kernel in front, a block asks for its first weights
 //    to be brought into L2: those do not depend on that kernel, and where they do
-//    (a quantization right before) L2 is where the new values appear.
+//    (a quantization right before) L2 is where the new values appear.  (One call after the
+//    other, 8 tokens: 5.5 us instead of 5.6 at 2048 x 8192, 7.3 instead of 7.5 at 8192 x
+//    4096; the smallest lose 0.1.)
+//
+// 32768 x 8192, groups of 128: 1 token 30.3 us, 8 31.0 (4.5 TB/s, 70 % of a copy), 16 45.5.
+// Large shapes are bound by the instructions that widen codes: issue slots 63 %, the
+// integer and logic pipe 59 % busy, the tensor pipe 26 %.  The same kernel with codes
+// used as they are takes 26.2, without its products 24.2.
 
-// Warps of a block: where two sets of columns double the sums, half as many with twice
-// the registers.
+// Warps of a block: 16 tiles of two sets of columns need twice the registers, and their sums
+// would not fit into shared memory 16 times.
 constexpr int gemv_warps(int RT, int NT) { return RT * NT > 16 ? 8 : 16; }
 // Tiles that a warp takes in one go: two, whose products do not depend on one another and
 // which share the waiting and counting, unless there is only one.
 constexpr int gemv_pair(int RT) { return RT > 1 ? 2 : 1; }
-constexpr int gemv_stages(int RT, int NT) { return 64 / gemv_warps(RT, NT) / gemv_pair(RT); }
+// The warps' rings hold 64 records together.  (96 and 128: 30.8 us instead of 31.0 for 8 tokens
+// at 32768 x 8192, 11.0 and 11.9 instead of 10.1 for one at 16384 x 4096: what is asked for at the start
+// has to arrive before the first product.)
+constexpr int kRingRecords = 64;
+constexpr int gemv_stages(int RT, int NT) { return kRingRecords / gemv_warps(RT, NT) / gemv_pair(RT); }
 
 struct GemvArgs {
   const uint16_t *X;
@@ -290,7 +301,6 @@ __global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(
   constexpr int kRecord = record_bytes(GROUP), kPair = gemv_pair(RT), kStage = kPair * kRecord;
   constexpr int kStages = gemv_stages(RT, NT), kGemvWarps = gemv_warps(RT, NT);
   constexpr int kCols = 8 * NT, kTileSums = 16 * kCols;
-  constexpr bool kAhead = RT * NT <= 4;             // registers for the next block's tokens
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int r = lane >> 2, c = lane & 3;
@@ -378,21 +388,12 @@ __global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) total[t][n][e] = 0.0f;
-    uint4 x[NT][4], ahead[NT][4];
-    if (kAhead && left > 0) load_x(ahead, kb);
+    uint4 x[NT][4];
     uint32_t stage = ring + 16 * lane;
     const int steps_at = 1024 + r * kScaleRow - 16 * lane;
     while (left > 0) {
       const int u1 = min(units, u0 + left);  // units u0 .. u1 - 1 of block kb
-      if (kAhead) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) x[n][j] = ahead[n][j];
-        if (left > u1 - u0) load_x(ahead, kb + 1);
-      } else {
-        load_x(x, kb);
-      }
+      load_x(x, kb);
 #pragma unroll
       for (int u = 0; u < RT / kPair; ++u) {
         if (u < u0 || u >= u1) continue;
@@ -532,7 +533,7 @@ w4a4_status launch_dequantize(const w4a4_group_weights_t *w, uint16_t *W, void *
 
 template <typename T, int GROUP, int RT, int NT>
 w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
-  constexpr int kGemvWarps = gemv_warps(RT, NT), kRing = 64 * record_bytes(GROUP);
+  constexpr int kGemvWarps = gemv_warps(RT, NT), kRing = kRingRecords * record_bytes(GROUP);
   constexpr int kSums = kGemvWarps * RT * 16 * 8 * NT * 4, kSmem = kRing > kSums ? kRing : kSums;
   static ContextCache<int> ready;  // per context: attribute set
   int done = 0;
@@ -549,15 +550,20 @@ w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
 
 template <typename T, int GROUP>
 w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
-  // as many tiles at a time as a block has, up to what its registers hold
+  // As many tiles at a time as a block has, in steps, up to what its registers hold; fewer at a time
+  // leave the ring more stages (us at N x K on 148 SMs, 8 or 16 tokens):
+  //   1 tile: alone 5.6 and 6.4, as 4 with three empty 6.7 and 8.1 (2048 x 8192)
+  //   2 to 4: up to 8 tokens 8 at a time are as good as 4 (7.2 both, 8192 x 4096); 16 tokens, 4 at a time 9.3, 8 10.7
+  //   5 to 8: 8 at a time 11.0 and 16.5, 16 11.6 and 17.4 (16384 x 4096)
+  //   more:   16 at a time 31.1 and 45.6, 16 tokens with 8 50.3, with 4 52.1 (32768 x 8192)
   const int tiles = (a.s.tiles - 1) / device_sm_count() + 1;
   if (a.M <= 8) {
     if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 1>(a, stream);
-    if (tiles <= 4) return launch_gemv_t<T, GROUP, 4, 1>(a, stream);
     return tiles <= 8 ? launch_gemv_t<T, GROUP, 8, 1>(a, stream) : launch_gemv_t<T, GROUP, 16, 1>(a, stream);
   }
   if (tiles == 1) return launch_gemv_t<T, GROUP, 1, 2>(a, stream);
-  return tiles <= 4 ? launch_gemv_t<T, GROUP, 4, 2>(a, stream) : launch_gemv_t<T, GROUP, 16, 2>(a, stream);
+  if (tiles <= 4) return launch_gemv_t<T, GROUP, 4, 2>(a, stream);
+  return tiles <= 8 ? launch_gemv_t<T, GROUP, 8, 2>(a, stream) : launch_gemv_t<T, GROUP, 16, 2>(a, stream);
 }
 
 }  // namespace
