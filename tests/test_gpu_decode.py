@@ -464,6 +464,17 @@ def test_attend_drawn(w4, seed):
     check_attend(w4, *case, window=pick(0, 0, 13, 64, 1000))
 
 
+@pytest.mark.parametrize("H,G", [(1, 4), (2, 1), (4, 2), (4, 12), (6, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_with_wide_tables(w4, D, H, G):
+    """The table's width is all the host knows of the lengths; results hold for any."""
+    q, cache, K, V, pages, lens = attend_case(w4, 8, [1, 700, 33, 0, 2500, 16, 15, 90], H * G, H, D, 16, "nhd", BF16, 26)
+    wide = torch.full((8, 1 << 14), -1, dtype=torch.int32)
+    wide[:, :pages.shape[1]] = pages
+    check_attend(w4, q, cache, K, V, pages, lens)
+    check_attend(w4, q, cache, K, V, wide, lens)
+
+
 def test_attend_very_many(w4):
     """More sequences than threads: every thread adds up a run of them."""
     lens = [(i * i) % 23 if i % 7 else 0 for i in range(1500)]

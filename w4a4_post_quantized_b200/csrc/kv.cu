@@ -178,20 +178,21 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //
 //  * The warps of a block take neighbouring cache heads (4, 2 or 1, by what divides
 //    their number) of the same tokens, so that a token's row is read in one go in whichever
-//    order the cache holds tokens and heads.  With each block on one head, caches
-//    ordered by token ran at 73 % of the copy rate where those ordered by head ran at 90.
-//  * The work of such a team is the concatenation, over sequences, groups of heads and chunks
-//    of up to 16 of the query heads that share one, of pieces of 16 tokens (of 32 at 64
-//    dims).  The lengths are on the device, so every block of a grid that fills the
-//    GPU once adds them up and each team takes an equal share of that line: a long
-//    sequence is split over as many teams as it needs, short ones share one.  A
-//    team finishes the items that lie inside its share; of an item that it shares with
-//    others it leaves maximum, sum and unnormalised output in the workspace (two at
-//    most: its first and its last), and kv_join_kernel joins those.
+//    order the cache holds tokens and heads; one head where rows are long and there is
+//    little to do (w4a4_kv_attend has the rule).
+//  * The work of such a team is the concatenation, over sequences, groups of heads and
+//    chunks of up to 16 of the query heads that share one, of pieces of 16 tokens (of 32 at
+//    64 dims; with 16 there 61.9 us instead of 57.6 for 64 frames).  The lengths are on the
+//    device, so every block of a grid that fills the GPU once adds them up and each team
+//    takes an equal share of that line: a long sequence is split over as many teams as it
+//    needs, short ones share one.  A team finishes the items that lie inside its share; of an
+//    item that it shares with others it leaves maximum, sum and unnormalised output in the
+//    workspace (two at most: its first and its last), and kv_join_kernel joins those.  A
+//    block whose teams all work on one item joins them first.
 //  * A warp works alone, through its own ring of stages filled by 16-byte asynchronous
-//    copies that run ahead across the ends of items: no block-wide wait anywhere.
-//    A piece that lies in one page is looked up once, one that does not row by row.  Rows without a token are filled with zeros by the copy
-//    itself.
+//    copies that run ahead across the ends of items: no block-wide wait anywhere.  A piece
+//    that lies in one page is looked up once, one that does not row by row.  Rows
+//    without a token are filled with zeros by the copy itself.
 //  * The products are m16n8k16 tensor-core instructions (a piece has at most 16
 //    rows of queries, so tcgen05's 128-row tiles would be nearly empty, and at
 //    HBM's pace these take a quarter of the tensor pipe).  Scores: A = queries (heads
@@ -205,10 +206,15 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //    as large as the rounding of the result.  The reference that is
 //    subtracted from the scores lies kTop below their maximum, so that in fp16 the
 //    small ones are not lost.
+//
+// us, and the share of a copy's rate: 64 frames of one sequence (87936 tokens, 16 heads of 64)
+// 57.4, 97 %; 64 sequences of 8192 127, 98 %; 23 of 1 to 4001 37.5, 78 %, where the wait for
+// the first lengths, pages and rows and the join are what is left; one frame (1374 tokens) 7.5,
+// all of it such waits.  In long ones issue slots are 34 %, the tensor pipe 21 % busy.
 
 constexpr int kAttendWarps = 4;
 constexpr int kMaxBlocks = 448;      // partial results in the workspace: two per warp
-constexpr int kChunk = 16;           // most query heads of a warp's item
+constexpr int kChunk = 16;           // most query heads of a warp's item (8: 66 us, not 54, for 16 sharing a head)
 constexpr float kLog2e = 1.4426950408889634f;
 
 constexpr int attend_piece(int D) { return D == 64 ? 32 : 16; }  // tokens of a stage: 8 KB of keys and values
@@ -315,6 +321,8 @@ __device__ __forceinline__ void write_out(const AttendArgs &a, int b, int h, int
   if (d == 0 && a.lse) a.lse[at] = log_sum(top, sum);
 }
 
+// Three blocks on an SM, two with the sums of 16 heads (168 registers a thread do not hold
+// those at 128 dims; at 64 three blocks gain nothing, 31.6 us and 31.8).
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     kv_attend_kernel(AttendArgs a, unsigned int *__restrict__ status) {
@@ -700,11 +708,13 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 
 // Joins the parts of every item that teams share, per head: a warp per item and head,
 // which leaves at once where one team held all of it; a block where there are more than
-// kManyParts (a quarter as many where every block has one job at most).  Which teams hold parts follows from the line, which each block works out
-// while the main kernel still runs.  A lane takes 4 dims of every kGroups-th part with its
-// own running maximum and sum, 8 parts in flight: after the wait one read remains.
-// (Lists of the shared items made by every block, or written by the main kernel, put
-// two or three more behind the wait; 7 to 11 us in all.)
+// kManyParts (a quarter as many where every block has one job at most).  (Warps only: 100000
+// tokens of one head 59 us instead of 23, one frame 9.4 instead of 7.6; blocks above 4 parts:
+// 64 sequences of 8192 132 instead of 127.)  Which teams hold parts follows from the line,
+// which each block works out while the main kernel still runs.  A lane takes 4 dims of
+// every kGroups-th part with its own running maximum and sum, 8 parts in flight: after the
+// wait one read remains.  (Lists of the shared items made by every block, or written by
+// the main kernel, put two or three more behind the wait; 7 to 11 us in all.)
 constexpr int kJoinWarps = 8;
 constexpr int kManyParts = 32;
 
@@ -1043,10 +1053,11 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
   cudaLaunchAttribute attr;
-  // shares of a token's heads (at most one per 4 passes of a warp) until there
-  // are 8 warps per SM
+  // shares of a token's heads (at most one per 4 passes of a warp) until there are 4 warps
+  // per SM (1 to 256 tokens of 48 heads: 3.1 us instead of 3.7 undivided; 10992 tokens: 26 undivided,
+  // 30 in shares; 1024 tokens: 4.1 undivided, 4.4 in shares)
   const int round = 4 * (32 / (D / 16)), most = (2 * Hk + Hq + round - 1) / round;
-  const int64_t want = (8ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
+  const int64_t want = (4ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
   const int parts = static_cast<int>(want < most ? want : most);
   const cudaLaunchConfig_t cfg =
       launch_config((t.n_tokens * parts + kAppendWarps - 1) / kAppendWarps, 32 * kAppendWarps, 0, stream, &attr);
@@ -1090,9 +1101,19 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   a.group = Hq / Hk;
   a.chunks = (a.group + kChunk - 1) / kChunk;
   a.chunk = (a.group + a.chunks - 1) / a.chunks;
-  a.team = Hk % 4 == 0 ? 4 : Hk % 2 == 0 ? 2 : 1;
+  const int64_t room = static_cast<int64_t>(t.max_pages) * a.cache.page_size;
+  // Neighbouring cache heads in a team, except where rows are long and there is little to do
+  // for each warp (as far as the host knows): then shares of single heads, whose parts a
+  // block joins by itself, win.  us with teams and without, 8 heads of 128: 1 sequence of 1024
+  // tokens 7.8 and 7.1, 23 of up to 4001 38.4 and 37.6; 64 of 2048 83.9 and 87.5, 16 of 16384
+  // 158.2 and 160.5.  Of 64 (16 heads, 64 of 2048, by token): 87.7 and 94.5.
+  const int64_t warps = 3 * kAttendWarps * device_sm_count();
+  if (D == 64 || (room / 16) * Hk * a.chunks >= 32 * warps / t.n_seqs)
+    a.team = Hk % 4 == 0 ? 4 : Hk % 2 == 0 ? 2 : 1;
+  else
+    a.team = 1;
   {  // the line of pieces is counted in 32 bits
-    const int64_t pieces = (static_cast<int64_t>(t.max_pages) * a.cache.page_size + 15) / 16;
+    const int64_t pieces = (room + 15) / 16;
     const int64_t items = static_cast<int64_t>(Hk / a.team) * a.chunks;
     if (items * pieces >= (int64_t(1) << 31) / t.n_seqs) return W4A4_ERR_SHAPE;
   }
