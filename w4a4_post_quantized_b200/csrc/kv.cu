@@ -75,18 +75,23 @@ __device__ __forceinline__ void load4(const float *from, float (&to)[8], int fir
 // takes a token (or one of `parts` shares of its heads, where tokens are too few to
 // fill the GPU).  A lane keeps two 16-byte pieces of the heads for good, where halves
 // turn the two that turn together, so the token's cosines and sines are read once into
-// registers, and goes over the heads in rounds of four whose loads are all in flight
-// before the first store, and before the page is known.  The pieces of
+// registers, and goes over the heads in rounds of append_round passes whose loads are all in
+// flight before the first store, and before the page is known.  The pieces of
 // neighbouring lanes are neighbours in memory: with each lane's two pieces side by side
 // every sector was written in two halves, 24.6 us instead of 22 for 5003 tokens of 128
 // dims turned in part.  (One block per token, thread by thread over its elements, took 67
-// us for 8 frames; now 26, and 94 % of the copy rate on four times as many tokens.)
-constexpr int kAppendWarps = 4;
+// us for 8 frames; now 25.0, 5.5 TB/s, and 78.6, 98 % of a copy's rate, on 40000 tokens.)
+constexpr int kAppendWarps = 2;
+
+// Passes of a round.  More are more loads in flight per warp, fewer leave registers for more
+// warps: 8 frames (64 dims, 48 heads) 26.8 us with 4, 25.1 with 3, 26.2 with 2; 4000 tokens of
+// 128 dims and 48 heads 22.4 with 4, 18.9 with 2.
+constexpr int append_round(int D) { return D == 64 ? 3 : 2; }
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kAppendWarps)
     kv_append_kernel(AppendArgs a, int64_t T_, int parts, unsigned int *__restrict__ status) {
-  constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kRound = 4;  // units of a head, heads of a pass
+  constexpr int kUnits = D / 16, kHeads = 32 / kUnits, kRound = append_round(D);  // units of a head, heads of a pass
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -1053,11 +1058,11 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
   cudaLaunchAttribute attr;
-  // shares of a token's heads (at most one per 4 passes of a warp) until there are 4 warps
-  // per SM (1 to 256 tokens of 48 heads: 3.1 us instead of 3.7 undivided; 10992 tokens: 26 undivided,
-  // 30 in shares; 1024 tokens: 4.1 undivided, 4.4 in shares)
-  const int round = 4 * (32 / (D / 16)), most = (2 * Hk + Hq + round - 1) / round;
-  const int64_t want = (4ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
+  // shares of a token's heads, at most one per round of a warp, up to about the 24 warps per SM that
+  // fit: 600 tokens of 128 dims and 48 heads 4.9 us (up to 16 warps 5.5, 4 8.9), 1000 6.4 (6.6, 9.2);
+  // 5003 19.4 undivided, 25.0 in as many shares as there are rounds
+  const int round = append_round(D) * (32 / (D / 16)), most = (2 * Hk + Hq + round - 1) / round;
+  const int64_t want = (24ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
   const int parts = static_cast<int>(want < most ? want : most);
   const cudaLaunchConfig_t cfg =
       launch_config((t.n_tokens * parts + kAppendWarps - 1) / kAppendWarps, 32 * kAppendWarps, 0, stream, &attr);
