@@ -26,9 +26,6 @@ struct GroupShape {
 // steps of rows r and r + 8, group by group.
 __host__ __device__ constexpr int record_bytes(int group) { return 1024 + 32 * (kBlockK / group); }
 
-// Nibble of element e (0..7) in a word: 0, 2, 4, 6, 1, 3, 5, 7 from the lowest up.
-__device__ __forceinline__ int nibble_shift(int e) { return 4 * ((e >> 1) + 4 * (e & 1)); }
-
 // ------------------------------------------------- quantize, pack, dequantize
 //
 // One pass over the weights, bound by HBM (2 bytes in, half a byte and the steps
@@ -166,12 +163,12 @@ __global__ void __launch_bounds__(32 * kPackWarps)
     uint32_t word[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t v = 0, w = 0;
+      uint32_t v = 0;
       if (n < s.N && u.k + 32 * j < s.K)
         v = *reinterpret_cast<const uint32_t *>(codes + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << nibble_shift(e);
-      word[j] = w;
+      // nibbles 0, 2, 4, 6 meet in bytes 0 and 2 of one word, 1, 3, 5, 7 in those of another
+      const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
+      word[j] = __byte_perm(even | (even >> 4), odd | (odd >> 4), 0x6420);
     }
     *reinterpret_cast<uint4 *>(record + 512 * h + 16 * lane) =
         make_uint4(word[0], word[1], word[2], word[3]);
