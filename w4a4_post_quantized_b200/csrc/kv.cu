@@ -198,6 +198,9 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //    copies that run ahead across the ends of items: no block-wide wait anywhere.  A piece
 //    that lies in one page is looked up once, one that does not row by row.  Rows
 //    without a token are filled with zeros by the copy itself.
+//  * Where the table leaves room for little (w4a4_kv_attend's launch has the rule), there is no line:
+//    one cluster of up to 8 blocks takes each item, a piece or a few per warp, and its
+//    blocks join their parts through distributed shared memory.  One launch instead of two.
 //  * The products are m16n8k16 tensor-core instructions (a piece has at most 16
 //    rows of queries, so tcgen05's 128-row tiles would be nearly empty, and at
 //    HBM's pace these take a quarter of the tensor pipe).  Scores: A = queries (heads
@@ -214,10 +217,11 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //
 // us, and the share of a copy's rate: 64 frames of one sequence (87936 tokens, 16 heads of 64)
 // 57.4, 97 %; 64 sequences of 8192 127, 98 %; 23 of 1 to 4001 37.5, 78 %, where the wait for
-// the first lengths, pages and rows and the join are what is left; one frame (1374 tokens) 7.5,
+// the first lengths, pages and rows and the join are what is left; one frame (1374 tokens) 7.2,
 // all of it such waits.  In long ones issue slots are 34 %, the tensor pipe 21 % busy.
 
 constexpr int kAttendWarps = 4;
+constexpr int kMaxCluster = 8;       // blocks of a cluster (8 is what every launch may ask for)
 constexpr int kMaxBlocks = 448;      // partial results in the workspace: two per warp
 constexpr int kChunk = 16;           // most query heads of a warp's item (8: 66 us, not 54, for 16 sharing a head)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -243,6 +247,7 @@ struct AttendArgs {
   uint16_t *out;
   float *lse;
   float *part;                       // [teams][2][team][chunk][D + 4]: output, maximum, sum
+  int cluster;                       // blocks that share an item, where the clusters' form runs
 
   // an item's group of heads and chunk
   __device__ __forceinline__ int heads_of(int item) const { return chunks == 1 ? item : item / chunks; }
@@ -312,6 +317,18 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// From another block's shared memory.
+__device__ __forceinline__ float4 ld_cluster16(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster8(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
+  return v;
+}
+
 // The logarithm of a sum of 2^x held as top and sum of 2^(x - top); top is any finite reference.
 __device__ __forceinline__ float log_sum(float top, float sum) {
   return sum == 0.0f ? -INFINITY : ((top == -INFINITY ? 0.0f : top) + log2f(sum)) * 0.69314718055994531f;
@@ -328,7 +345,10 @@ __device__ __forceinline__ void write_out(const AttendArgs &a, int b, int h, int
 
 // Three blocks on an SM, two with the sums of 16 heads (168 registers a thread do not hold
 // those at 128 dims; at 64 three blocks gain nothing, 31.6 us and 31.8).
-template <typename T, int D, int NT>
+//
+// CLUSTER: an item is shared by the warps of one cluster of blocks, which join their parts
+// through shared memory: one launch and no line, for calls with little to do.
+template <typename T, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     kv_attend_kernel(AttendArgs a, unsigned int *__restrict__ status) {
   constexpr int P = attend_piece(D);
@@ -352,77 +372,96 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   const int teams_here = kAttendWarps / a.team;
   const int team = blockIdx.x * teams_here + warp / a.team, member = warp % a.team;
 
-  // The line of pieces.  Up to 32 sequences every warp adds up for itself, one per lane;
-  // of more, every thread of the block adds up a run.
-  const bool few = B <= 32;
-  const int run = few ? 1 : (B + 127) / 128, run0 = few ? lane : tid * run;
-  int mine = 0;
-  for (int i = run0; i < min(B, run0 + run); ++i) {
-    const Range<P> v(a, i);
-    if (blockIdx.x == 0 && a.lens[i] > v.end) atomicOr(status, W4A4_DEV_RANGE);
-    mine += v.pieces * per_seq;
-  }
-  int upto = mine;
-  for (int o = 1; o < min(B, 32); o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += v;
-  }
-  int total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
-  if (!few) {
-    if (lane == 31) sums[warp] = upto;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < kAttendWarps; ++w) {
-      if (w < warp) upto += sums[w];
-      total += sums[w];
-    }
-  }
-  const Shares shares(total, gridDim.x * teams_here);
-  const int begin = shares.begin(team);
-  int left = team < shares.teams ? shares.begin(team + 1) - begin : 0;
-  // The sequence that the share begins in, and where that begins.
-  int b = 0;
-  int off = 0;  // of the share in it
-  if (few) {
-    if (left) {
-      b = __ffs(__ballot_sync(0xffffffffu, begin < upto)) - 1;
-      off = begin - __shfl_sync(0xffffffffu, upto - mine, b);
-    }
+  int b = 0, begin = 0, left = 0;              // the share's first sequence, place in the line, pieces
+  int item = 0, piece = 0;                     // of that sequence, of that item: where it begins
+  bool merged = false;                         // the block's teams all work on one item, and leave one part
+  const int team0 = blockIdx.x * teams_here;
+  if constexpr (CLUSTER) {
+    const int index = blockIdx.x / a.cluster, w = (blockIdx.x - index * a.cluster) * kAttendWarps + warp;
+    b = index / per_seq;
+    item = index - b * per_seq;
+    const Range<P> v(a, b);
+    if (w == 0 && item == 0 && lane == 0 && a.lens[b] > v.end) atomicOr(status, W4A4_DEV_RANGE);
+    const int warps = kAttendWarps * a.cluster, each = v.pieces / warps, more = v.pieces - each * warps;
+    piece = w * each + min(w, more);
+    left = each + (w < more ? 1 : 0);
   } else {
-    for (int t = 0; t < teams_here; ++t) {
-      const int from = shares.begin(blockIdx.x * teams_here + t);
-      if (upto - mine <= from && from < upto) {
-        int at = upto - mine;
-        int i = run0;
-        for (;; ++i) {
-          const int n = Range<P>(a, i).pieces * per_seq;
-          if (from < at + n) break;
-          at += n;
-        }
-        found[t][0] = at;
-        found[t][1] = i;
+    // The line of pieces.  Up to 32 sequences every warp adds up for itself, one per lane;
+    // of more, every thread of the block adds up a run.
+    const bool few = B <= 32;
+    const int run = few ? 1 : (B + 127) / 128, run0 = few ? lane : tid * run;
+    int mine = 0;
+    for (int i = run0; i < min(B, run0 + run); ++i) {
+      const Range<P> v(a, i);
+      if (blockIdx.x == 0 && a.lens[i] > v.end) atomicOr(status, W4A4_DEV_RANGE);
+      mine += v.pieces * per_seq;
+    }
+    int upto = mine;
+    for (int o = 1; o < min(B, 32); o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += v;
+    }
+    int total = __shfl_sync(0xffffffffu, upto, min(B, 32) - 1);
+    if (!few) {
+      if (lane == 31) sums[warp] = upto;
+      __syncthreads();
+      total = 0;
+      for (int w = 0; w < kAttendWarps; ++w) {
+        if (w < warp) upto += sums[w];
+        total += sums[w];
       }
     }
-    __syncthreads();
-    if (left) {
-      off = begin - found[warp / a.team][0];
-      b = found[warp / a.team][1];
+    const Shares shares(total, gridDim.x * teams_here);
+    begin = shares.begin(team);
+    left = team < shares.teams ? shares.begin(team + 1) - begin : 0;
+    // The sequence that the share begins in, and where that begins.
+    int off = 0;  // of the share in it
+    if (few) {
+      if (left) {
+        b = __ffs(__ballot_sync(0xffffffffu, begin < upto)) - 1;
+        off = begin - __shfl_sync(0xffffffffu, upto - mine, b);
+      }
+    } else {
+      for (int t = 0; t < teams_here; ++t) {
+        const int from = shares.begin(blockIdx.x * teams_here + t);
+        if (upto - mine <= from && from < upto) {
+          int at = upto - mine;
+          int i = run0;
+          for (;; ++i) {
+            const int n = Range<P>(a, i).pieces * per_seq;
+            if (from < at + n) break;
+            at += n;
+          }
+          found[t][0] = at;
+          found[t][1] = i;
+        }
+      }
+      __syncthreads();
+      if (left) {
+        off = begin - found[warp / a.team][0];
+        b = found[warp / a.team][1];
+      }
     }
+    // Nothing to attend to: zeros, spread over the warps.
+    for (int i = blockIdx.x * kAttendWarps + warp; i < B; i += gridDim.x * kAttendWarps)
+      if (Range<P>(a, i).pieces == 0) {
+        for (int j = lane; j < a.q_heads * D / 8; j += 32)
+          reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(i) * a.q_heads * D)[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse)
+          for (int j = lane; j < a.q_heads; j += 32) a.lse[static_cast<int64_t>(i) * a.q_heads + j] = -INFINITY;
+      }
+    if (left == 0) return;
+    const int pieces = Range<P>(a, b).pieces;
+    item = off / pieces;
+    piece = off - item * pieces;
+    const int item_at = begin - piece;
+    merged = teams_here > 1 && team0 + teams_here <= shares.teams && item_at <= shares.begin(team0) &&
+             shares.begin(team0 + teams_here) <= item_at + pieces;
   }
-  // Nothing to attend to: zeros, spread over the warps.
-  for (int i = blockIdx.x * kAttendWarps + warp; i < B; i += gridDim.x * kAttendWarps)
-    if (Range<P>(a, i).pieces == 0) {
-      for (int j = lane; j < a.q_heads * D / 8; j += 32)
-        reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(i) * a.q_heads * D)[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (a.lse)
-        for (int j = lane; j < a.q_heads; j += 32) a.lse[static_cast<int64_t>(i) * a.q_heads + j] = -INFINITY;
-    }
-  if (left == 0) return;
 
   // ---- the copies' side: the next piece to look up, then its rows
   Range<P> cr(a, b);
-  int cb = b, citem = off / cr.pieces, cpiece = off - citem * cr.pieces, cleft = left;
-  int item = citem, piece = cpiece;            // the products' side starts there too
+  int cb = b, citem = item, cpiece = piece, cleft = left;
   Range<P> range = cr;
   const int64_t values = a.cache.v - a.cache.k;
   const int crow = lane / kPieces, cpos = lane % kPieces;
@@ -509,11 +548,6 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
   }
 
   // ---- the products' side
-  // Where the block has several teams and all of them work on one item, they leave one part.
-  const int team0 = blockIdx.x * teams_here;
-  const int item_at = begin - piece;
-  const bool merged = teams_here > 1 && team0 + teams_here <= shares.teams && item_at <= shares.begin(team0) &&
-                      shares.begin(team0 + teams_here) <= item_at + range.pieces;
   int stage = 0;
   bool at_begin = true;
   while (left > 0) {
@@ -644,7 +678,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
 
     // The item, or this team's part of it, is done.  A lane holds dims 64 j + 8 r .. + 7 of
     // heads 2 c and 2 c + 1 (+ 8 n).
-    const bool whole_item = !merged && piece == 0 && n_here == range.pieces;
+    const bool whole_item = !CLUSTER && !merged && piece == 0 && n_here == range.pieces;
     const int slot = at_begin ? 0 : 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -667,7 +701,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
                            T::pack(acc[n][4 * j + 3][e] * inv, acc[n][4 * j + 3][2 + e] * inv));
           if (r == 0 && a.lse) a.lse[at] = log_sum(top, sum);
         } else {
-          float *p = merged ? reinterpret_cast<float *>(smem + warp * kStages * kStage) + h * kPart
+          float *p = CLUSTER || merged ? reinterpret_cast<float *>(smem + warp * kStages * kStage) + h * kPart
                             : a.part + (((static_cast<int64_t>(team) * 2 + slot) * a.team + member) * a.chunk + h) * kPart;
 #pragma unroll
           for (int j = 0; j < D / 64; ++j) {
@@ -685,6 +719,56 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     piece += n_here;
   }
   if (absent) atomicOr(status, W4A4_DEV_RANGE);
+  if constexpr (CLUSTER) {
+    const int h0 = a.chunk_of(item) * a.chunk, heads = min(a.chunk, a.group - h0);
+    auto part = [&](int t, int h) { return smem + (t % kAttendWarps) * kStages * kStage + h * kPart * 4; };
+    if (at_begin && lane < heads)  // no share
+      *reinterpret_cast<float2 *>(part(warp, lane) + 4 * D) = make_float2(-INFINITY, 0.0f);
+    __syncwarp();
+    cluster_sync();
+    // Block `rank` writes dims rank * 4 q .. + 4 q - 1 of every head, a warp per head: lane t has the
+    // weight of part t, lanes j of q the dims 4 j of every kGroups-th part.
+    const int rank = cluster_ctarank(), q = D / 4 / a.cluster, groups = 32 / q;
+    const int j = lane % q, g = lane / q, d = 4 * (rank * q + j);
+    for (int h = warp; h < heads; h += kAttendWarps) {
+      float2 ml = make_float2(-INFINITY, 0.0f);
+      if (lane < kAttendWarps * a.cluster) ml = ld_cluster8(cluster_addr(part(lane, h) + 4 * D, lane / kAttendWarps));
+      float4 v[D / 32];
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int t = g + i * groups;
+        v[i] = ld_cluster16(cluster_addr(part(t, h) + 4 * d, t / kAttendWarps));
+      }
+      float top = ml.x;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float f = exp2f(ml.x - (top == -INFINITY ? 0.0f : top));
+      float sum = ml.y == 0.0f ? 0.0f : f * ml.y;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      float4 o4 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        const int t = g + i * groups;
+        const float w = __shfl_sync(0xffffffffu, f, t);
+        if (w != 0.0f) {  // what an empty part holds may be anything
+          o4.x = fmaf(w, v[i].x, o4.x);
+          o4.y = fmaf(w, v[i].y, o4.y);
+          o4.z = fmaf(w, v[i].z, o4.z);
+          o4.w = fmaf(w, v[i].w, o4.w);
+        }
+      }
+      for (int o = q; o < 32; o <<= 1) {
+        o4.x += __shfl_xor_sync(0xffffffffu, o4.x, o);
+        o4.y += __shfl_xor_sync(0xffffffffu, o4.y, o);
+        o4.z += __shfl_xor_sync(0xffffffffu, o4.z, o);
+        o4.w += __shfl_xor_sync(0xffffffffu, o4.w, o);
+      }
+      if (lane < q) write_out<T, D>(a, b, a.heads_of(item) * a.group + h0 + h, d, o4, top, sum);
+    }
+    __syncwarp();
+    cluster_sync();  // no block leaves while another reads its shared memory
+  } else
   if (merged) {  // the same for every warp of the block; the rings hold the teams' parts
     __syncthreads();
     const int first = team - team0;                        // this warp joins heads first, first + teams_here, ...
@@ -939,7 +1023,8 @@ bool out_in_q(const uint16_t *q, int64_t stride, int64_t rows, int64_t row, cons
   return !(q == out && (rows == 1 || stride == row)) && overlap(q, rows, row, stride, out, rows * row);
 }
 
-cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr) {
+cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *stream, cudaLaunchAttribute *attr,
+                                 int cluster = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
   cfg.blockDim = dim3(threads, 1, 1);
@@ -949,6 +1034,12 @@ cudaLaunchConfig_t launch_config(int64_t grid, int threads, size_t smem, void *s
   attr->val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if (cluster) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
   return cfg;
 }
 
@@ -957,37 +1048,68 @@ size_t part_bytes(int group, int D) {
   return static_cast<size_t>(kMaxBlocks) * kAttendWarps * 2 * chunk * (D + 4) * sizeof(float);
 }
 
+// Blocks of a kernel per SM, once per context; 0 when it cannot run.
+template <typename T, int D, int NT, bool CLUSTER>
+int attend_blocks(int smem) {
+  static ContextCache<int> occupancy;
+  int per_sm = 0;
+  const cudaError_t e = occupancy.get(&per_sm, [smem](int *v) {
+    cudaError_t r = cudaFuncSetAttribute(kv_attend_kernel<T, D, NT, CLUSTER>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r == cudaSuccess)
+      r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kv_attend_kernel<T, D, NT, CLUSTER>, 32 * kAttendWarps, smem);
+    return r;
+  });
+  return e == cudaSuccess ? per_sm : 0;
+}
+
 template <typename T, int D, int NT>
 w4a4_status launch_attend(AttendArgs &a, void *stream) {
   constexpr int P = attend_piece(D), kSmem = kAttendWarps * kAttendStages * 2 * P * 2 * D;
-  static ContextCache<int> occupancy;  // per context: attribute set, blocks per SM
-  int per_sm = 0;
-  if (occupancy.get(&per_sm, [](int *v) {
-        cudaError_t e = cudaFuncSetAttribute(kv_attend_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             kSmem);
-        if (e == cudaSuccess)
-          e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kv_attend_kernel<T, D, NT>, 32 * kAttendWarps, kSmem);
-        return e;
-      }) != cudaSuccess || per_sm < 1)
-    return W4A4_ERR_CUDA;
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
+  const int64_t pieces = (static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size + P - 1) / P;
+  cudaLaunchAttribute attr[2];
+  {
+    // Clusters of as many blocks for an item as fit on the GPU and have a piece for every warp, where
+    // no warp gets many, as far as the host knows: 4; 1 where few items leave most of the GPU to
+    // a finer cut; 12 where blocks of long rows fill half of it.  us with clusters and with the
+    // line: 16 heads of 64, 1 sequence of 128 4.1 and 5.6, 1 of 1374 7.2 and 7.6, 16 of 500 11.6 and 14.1,
+    // of 1374 (11 pieces a warp) 25.1 and 22.9; 8 heads of 128: 1 of 500 5.3 and 6.2, 1 of 4096 (8) 12.1 and
+    // 11.2, 16 of 1374 (11, half the GPU) 20.6 and 23.1; 1 head of 64 for 8, 1 of 1374 7.4 and 6.8, 8 of 4096
+    // (8 items) 11.2 and 9.6.  (A launch as clusters takes 0.8 us more: one block per item goes without.)
+    const int per_sm = attend_blocks<T, D, NT, true>(kSmem);
+    if (per_sm < 1) return W4A4_ERR_CUDA;
+    const int64_t places = static_cast<int64_t>(device_sm_count()) * per_sm;
+    const int64_t items = static_cast<int64_t>(a.pages.n_seqs) * a.cache.heads * a.chunks;
+    int cluster = kMaxCluster;
+    while (cluster > 1 && (items * cluster > places || pieces <= kAttendWarps * (cluster / 2))) cluster /= 2;
+    const int most = items < 16 ? 1 : D == 128 && 2 * items * cluster >= places ? 12 : 4;
+    if (pieces > 1 && items * cluster <= places && pieces <= most * kAttendWarps * cluster) {
+      AttendArgs own = a;
+      own.team = 1;
+      own.cluster = cluster;
+      const cudaLaunchConfig_t cfg =
+          launch_config(items * cluster, 32 * kAttendWarps, kSmem, stream, attr, cluster > 1 ? cluster : 0);
+      return launch_status(cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT, true>, own, status));
+    }
+  }
+  const int per_sm = attend_blocks<T, D, NT, false>(kSmem);
+  if (per_sm < 1) return W4A4_ERR_CUDA;
   // blocks: one per place on the GPU, fewer when there cannot be that many pieces
   const int teams_here = kAttendWarps / a.team;
   int64_t grid = static_cast<int64_t>(device_sm_count()) * per_sm;
   if (grid > kMaxBlocks) grid = kMaxBlocks;
   const int64_t most = grid * teams_here;
-  const int64_t pieces = (static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size + P - 1) / P;
   const int64_t items = static_cast<int64_t>(a.pages.n_seqs) * (a.cache.heads / a.team) * a.chunks;
   if (pieces < most && items < most && items * pieces < most) grid = (items * pieces + teams_here - 1) / teams_here;
   if (grid < 1) grid = 1;
   const int teams = static_cast<int>(grid) * teams_here;
-  cudaLaunchAttribute attr;
-  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, &attr);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT>, a, status);
+  cudaLaunchConfig_t cfg = launch_config(grid, 32 * kAttendWarps, kSmem, stream, attr);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kv_attend_kernel<T, D, NT, false>, a, status);
   // one team, or items of one piece: nothing is shared
   if (e != cudaSuccess || teams == 1 || pieces <= 1) return launch_status(e);
-  cfg = launch_config(2 * device_sm_count(), 32 * kJoinWarps, 0, stream, &attr);
+  cfg = launch_config(2 * device_sm_count(), 32 * kJoinWarps, 0, stream, attr);
   return launch_status(cudaLaunchKernelEx(&cfg, kv_join_kernel<T, D>, a, teams));
 }
 
