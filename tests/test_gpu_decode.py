@@ -525,6 +525,16 @@ def test_attend_in_place_and_into_the_gaps_of_q(w4):
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("D,H,G", [(64, 16, 1), (128, 2, 4), (128, 8, 1)])
+@pytest.mark.parametrize("window", [1, 2, 17, 18, 33, 34, 300])
+def test_attend_windows_at_every_place_of_a_piece(w4, window, D, H, G):
+    """The most pieces that a window can touch decide how the work is cut."""
+    lens = [window - 1, window, window + 1] + [640 + i for i in range(33)]
+    q, cache, K, V, pages, lens = attend_case(w4, len(lens), lens, H * G, H, D, 16, "nhd", BF16, 27)
+    check_attend(w4, q, cache, K, V, pages, lens, window)
+    check_attend(w4, q[:2], cache, K, V, pages[:2], lens[:2], window)
+
+
 @pytest.mark.parametrize("page", [7, 16, 64])
 def test_attend_window_over_freed_pages(w4, page):
     """Pages that lie wholly in front of the window need not be there."""

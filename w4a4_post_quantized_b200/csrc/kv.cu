@@ -3,6 +3,7 @@
 // cached.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -1068,7 +1069,9 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   constexpr int P = attend_piece(D), kSmem = kAttendWarps * kAttendStages * 2 * P * 2 * D;
   unsigned int *status = nullptr;
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
-  const int64_t pieces = (static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size + P - 1) / P;
+  // most pieces of a sequence: of the table's room, or of a window that begins with a piece's last token
+  int64_t pieces = (static_cast<int64_t>(a.pages.max_pages) * a.cache.page_size + P - 1) / P;
+  if (a.window) pieces = std::min<int64_t>(pieces, (static_cast<int64_t>(a.window) + P - 2) / P + 1);
   cudaLaunchAttribute attr[2];
   {
     // Clusters of as many blocks for an item as fit on the GPU and have a piece for every warp, where
