@@ -152,8 +152,10 @@ typedef struct {
  * rot_dim = 0 are copied.
  *   - A negative pos[t] marks a padding token: nothing of it is read or written.
  *   - Two tokens of one call must not name the same row of a page: which one stays is
- *     not defined.  A cache whose pages, rows or heads share memory (a stride of 0
- *     over more than one) is refused (W4A4_ERR_SHAPE).
+ *     not defined.  A cache whose neighbouring pages, rows or heads share memory (a stride
+ *     below head_dim over more than one) is refused (W4A4_ERR_SHAPE), and so is one whose
+ *     v begins within a head of its k (W4A4_ERR_ARG).  Other strides are not looked into: no
+ *     two rows that a call writes may share memory, and k, v, q and q_out must not lie in them.
  *   - Strides are multiples of 8, at least n_heads * head_dim (q: n_q_heads * head_dim).
  *     rot_dim: a multiple of 16, at most head_dim.  n_tokens < 2^31; n_seqs <= 2^24; n_seqs *
  *     max_pages < 2^31. */

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_abi_decode import A, ARG, AppendT, CacheT, lib  # noqa: F401  (lib: the library as a fixture)
+from test_abi_decode import A, ARG, SHAPE, AppendT, CacheT, lib  # noqa: F401  (lib: the library as a fixture)
 
 FAR = 1 << 40  # addresses of arrays that take no part
 
@@ -28,3 +28,20 @@ def test_append_queries_over_keys_or_values(lib, name):  # noqa: F811
                          pos=7 * FAR, n_seqs=5, max_pages=3, n_q_heads=Hq)
                 a.update({name: A + (1 << 20), f"{name}_stride": stride, "q_out": A + (1 << 20) + 2 * at})
                 assert lib.w4a4_kv_append(cache(), ctypes.byref(AppendT(**a)), None) == ARG, (stride, at)
+
+
+def append_to(lib, **kw):  # noqa: F811
+    a = dict(k=FAR, v=2 * FAR, k_stride=256, v_stride=256, n_tokens=3, pages=6 * FAR, pos=7 * FAR, n_seqs=5, max_pages=3)
+    return lib.w4a4_kv_append(cache(**kw), ctypes.byref(AppendT(**a)), None)
+
+
+@pytest.mark.parametrize("name", ["stride_page", "stride_token", "stride_head"])
+def test_append_to_rows_that_share_memory(lib, name):  # noqa: F811
+    """Neighbours less than a head apart: what one token writes, another overwrites in part."""
+    for stride in range(0, 64, 8):
+        assert append_to(lib, **{name: stride}) == SHAPE, stride
+
+
+def test_append_to_keys_that_are_the_values(lib):  # noqa: F811
+    for at in range(-64 + 8, 64, 8):
+        assert append_to(lib, k=4 * FAR, v=4 * FAR + 2 * at) == ARG, at

@@ -1150,8 +1150,8 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   if (t.n_tokens < 0 || t.n_tokens >= (int64_t(1) << 31) || t.n_table < 0 || (t.q && (Hq < 1 || Hq > 65535)))
     return W4A4_ERR_SHAPE;
   if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
-  if ((a.cache.n_pages > 1 && a.cache.stride_page == 0) || (a.cache.page_size > 1 && a.cache.stride_token == 0) ||
-      (Hk > 1 && a.cache.stride_head == 0))
+  if ((a.cache.n_pages > 1 && a.cache.stride_page < D) || (a.cache.page_size > 1 && a.cache.stride_token < D) ||
+      (Hk > 1 && a.cache.stride_head < D))
     return W4A4_ERR_SHAPE;
   if (t.n_tokens == 0) return W4A4_OK;
   if (!t.k || !t.v || !t.pos || (t.q && !t.q_out) || (t.rot_dim && t.n_table && !t.table)) return W4A4_ERR_ARG;
@@ -1162,6 +1162,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
       !ptr_aligned16(t.table) || !ptr_aligned4(t.seq) || !ptr_aligned4(t.pos) || !ptr_aligned4(t.table_pos) ||
       t.k_stride % 8 || t.v_stride % 8 || (t.q && t.q_stride % 8))
     return W4A4_ERR_ALIGN;
+  if (overlap(a.cache.k, 1, D, 0, a.cache.v, D)) return W4A4_ERR_ARG;
   if (t.q) {  // a token's heads are spread over warps, which read and write in no order
     const int64_t q_row = static_cast<int64_t>(Hq) * D, kv_row = static_cast<int64_t>(Hk) * D;
     if (out_in_q(t.q, t.q_stride, t.n_tokens, q_row, t.q_out) ||
