@@ -1162,7 +1162,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
       !ptr_aligned16(t.table) || !ptr_aligned4(t.seq) || !ptr_aligned4(t.pos) || !ptr_aligned4(t.table_pos) ||
       t.k_stride % 8 || t.v_stride % 8 || (t.q && t.q_stride % 8))
     return W4A4_ERR_ALIGN;
-  if (overlap(a.cache.k, 1, D, 0, a.cache.v, D)) return W4A4_ERR_ARG;
+  if (a.cache.n_pages && overlap(a.cache.k, 1, D, 0, a.cache.v, D)) return W4A4_ERR_ARG;
   if (t.q) {  // a token's heads are spread over warps, which read and write in no order
     const int64_t q_row = static_cast<int64_t>(Hq) * D, kv_row = static_cast<int64_t>(Hk) * D;
     if (out_in_q(t.q, t.q_stride, t.n_tokens, q_row, t.q_out) ||
