@@ -75,7 +75,9 @@ size_t w4a4_group_weights_bytes(int32_t N, int32_t K, int32_t group);
 w4a4_status w4a4_group_bind(void *base, size_t bytes, int32_t N, int32_t K, int32_t group, uint32_t flags,
                             w4a4_group_weights_t *out);
 
-/* [PTQ] per group: s = round16(max|W| / 7), c = clamp(round-half-even(W / s),
+/* The inputs of these three must not overlap the output (W4A4_ERR_ARG).
+ *
+ * [PTQ] per group: s = round16(max|W| / 7), c = clamp(round-half-even(W / s),
  * -8, 7); a group with s = 0 gets zero codes.  W [N, K] 16-bit, finite. */
 w4a4_status w4a4_group_quantize(const uint16_t *W, const w4a4_group_weights_t *w, void *stream);
 
@@ -95,7 +97,7 @@ w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, vo
  * 16-bit or NULL.  Products of codes and activations are exact, sums are fp32:
  * per group first, then times the step.  flags: 0, or W4A4_FLAG_GELU_OUT (bf16
  * only): Y = bf16(GELU(y)) of the rounded y, as in w4a4_linear_ex.  Y must not
- * overlap X (W4A4_ERR_ARG). */
+ * overlap X, bias or the weights (W4A4_ERR_ARG). */
 w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weights_t *w, const uint16_t *bias,
                             uint16_t *Y, uint32_t flags, void *stream);
 

@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_abi_decode import A, ARG, SHAPE, AppendT, CacheT, lib  # noqa: F401  (lib: the library as a fixture)
+from test_abi_decode import A, ARG, SHAPE, AppendT, CacheT, GroupT, lib  # noqa: F401  (lib: the library as a fixture)
 
 FAR = 1 << 40  # addresses of arrays that take no part
 
@@ -45,3 +45,30 @@ def test_append_to_rows_that_share_memory(lib, name):  # noqa: F811
 def test_append_to_keys_that_are_the_values(lib):  # noqa: F811
     for at in range(-64 + 8, 64, 8):
         assert append_to(lib, k=4 * FAR, v=4 * FAR + 2 * at) == ARG, at
+
+
+def around(bytes_out, bytes_in, step=16):
+    """Every offset at which an output of some bytes meets an input of others, and a few that only touch its ends."""
+    ends = {s * step + o for s in range(2) for o in (-bytes_out + step, bytes_in - 2 * step)}
+    return sorted({o for o in ends | {0, -step, step} if -bytes_out < o < bytes_in})
+
+
+def test_group_products_over_what_they_read(lib):  # noqa: F811
+    """Results over tokens, bias or weights; results of the conversions over their inputs."""
+    N, K, group, M = 256, 512, 64, 3
+    packed = lib.w4a4_group_weights_bytes(N, K, group)
+    w = ctypes.byref(GroupT(N, K, group, 0, 2 * FAR))
+    for at in around(2 * M * N, 2 * M * K):
+        assert lib.w4a4_group_gemv(FAR, M, w, None, FAR + at, 0, None) == ARG, at
+    for at in around(2 * M * N, 2 * N):
+        assert lib.w4a4_group_gemv(FAR, M, w, 3 * FAR, 3 * FAR + at, 0, None) == ARG, at
+    for at in around(2 * M * N, packed):
+        assert lib.w4a4_group_gemv(FAR, M, w, None, 2 * FAR + at, 0, None) == ARG, at
+    for at in around(packed, 2 * N * K):
+        assert lib.w4a4_group_quantize(2 * FAR - at, w, None) == ARG, at
+    for at in around(packed, N * K // 2):
+        assert lib.w4a4_group_pack(2 * FAR - at, FAR, w, None) == ARG, at
+    for at in around(packed, 2 * N * (K // group)):
+        assert lib.w4a4_group_pack(FAR, 2 * FAR - at, w, None) == ARG, at
+    for at in around(2 * N * K, packed):
+        assert lib.w4a4_group_dequantize(w, 2 * FAR + at, None) == ARG, at

@@ -131,6 +131,11 @@ inline bool overlap(const uint16_t *a, int64_t rows, int64_t row, int64_t stride
   const int64_t t = at < row || stride == 0 ? 0 : (at - row) / stride + 1;
   return t < rows && t * stride + row > at && t * stride < at + n;
 }
+// Whether n bytes at a and m bytes at b share any.
+inline bool overlap_bytes(const void *a, size_t n, const void *b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < n : x - y < m;
+}
 inline w4a4_status launch_status(cudaError_t e) { return e == cudaSuccess ? W4A4_OK : W4A4_ERR_CUDA; }
 
 }  // namespace

@@ -481,6 +481,9 @@ GroupShape shape_of(int32_t N, int32_t K, int32_t group) {
   return {N, K, group, (N - 1) / kTileRows + 1, (K + kBlockK - 1) / kBlockK};
 }
 
+size_t weight_bytes(const w4a4_group_weights_t *w) { return 2 * static_cast<size_t>(w->N) * w->K; }
+size_t packed_bytes(const w4a4_group_weights_t *w) { return w4a4_group_weights_bytes(w->N, w->K, w->group); }
+
 w4a4_status check_group(const w4a4_group_weights_t *w) {
   if (!w) return W4A4_ERR_ARG;
   if (!group_ok(w->group) || (w->flags & ~kGroupFlags)) return W4A4_ERR_UNSUPPORTED;
@@ -597,6 +600,7 @@ w4a4_status w4a4_group_quantize(const uint16_t *W, const w4a4_group_weights_t *w
   if (st != W4A4_OK) return st;
   if (!W) return W4A4_ERR_ARG;
   if (!ptr_aligned16(W)) return W4A4_ERR_ALIGN;
+  if (overlap_bytes(W, weight_bytes(w), w->data, packed_bytes(w))) return W4A4_ERR_ARG;
   return (w->flags & W4A4_FLAG_FP16) ? launch_quantize<Fp16>(W, w, stream) : launch_quantize<Bf16>(W, w, stream);
 }
 
@@ -607,6 +611,9 @@ w4a4_status w4a4_group_pack(const uint8_t *codes, const uint16_t *scales, const 
   if (st != W4A4_OK) return st;
   if (!codes || !scales) return W4A4_ERR_ARG;
   if (!ptr_aligned16(codes) || !ptr_aligned16(scales)) return W4A4_ERR_ALIGN;
+  if (overlap_bytes(codes, weight_bytes(w) / 4, w->data, packed_bytes(w)) ||
+      overlap_bytes(scales, weight_bytes(w) / w->group, w->data, packed_bytes(w)))
+    return W4A4_ERR_ARG;
   const GroupShape s = shape_of(w->N, w->K, w->group);
   return launch_status(
       launch(group_pack_kernel, pack_grid(s), 32 * kPackWarps, 0, stream, codes, scales, s, w->data));
@@ -618,6 +625,7 @@ w4a4_status w4a4_group_dequantize(const w4a4_group_weights_t *w, uint16_t *W, vo
   if (st != W4A4_OK) return st;
   if (!W) return W4A4_ERR_ARG;
   if (!ptr_aligned16(W)) return W4A4_ERR_ALIGN;
+  if (overlap_bytes(W, weight_bytes(w), w->data, packed_bytes(w))) return W4A4_ERR_ARG;
   return (w->flags & W4A4_FLAG_FP16) ? launch_dequantize<Fp16>(w, W, stream) : launch_dequantize<Bf16>(w, W, stream);
 }
 
@@ -632,7 +640,10 @@ w4a4_status w4a4_group_gemv(const uint16_t *X, int64_t M, const w4a4_group_weigh
   if (M == 0) return W4A4_OK;
   if (!X || !Y) return W4A4_ERR_ARG;
   if (!ptr_aligned16(X) || !ptr_aligned16(Y) || (bias && !ptr_aligned16(bias))) return W4A4_ERR_ALIGN;
-  if (overlap(X, 1, M * w->K, 0, Y, M * w->N)) return W4A4_ERR_ARG;
+  const size_t y_bytes = 2 * static_cast<size_t>(M) * w->N;
+  if (overlap_bytes(X, 2 * static_cast<size_t>(M) * w->K, Y, y_bytes) || overlap_bytes(w->data, packed_bytes(w), Y, y_bytes) ||
+      (bias && overlap_bytes(bias, 2 * static_cast<size_t>(w->N), Y, y_bytes)))
+    return W4A4_ERR_ARG;
   const GemvArgs a{X, static_cast<int>(M), w->data, shape_of(w->N, w->K, w->group), bias, Y, gelu, 0};
   switch (w->group) {
     case 32: return fp16 ? launch_gemv<Fp16, 32>(a, stream) : launch_gemv<Bf16, 32>(a, stream);
