@@ -193,8 +193,9 @@ typedef struct {
  *     whatever they hold, nor are the pages that hold only such rows.  Pages may be shared
  *     between sequences.  An infinite value of a token that is attended to gives an infinity
  *     or NaN in its dimension (of the heads that share it); keys follow the formula.
- *   - out may be q itself when q_stride = n_q_heads * head_dim, and must not overlap it
- *     otherwise (W4A4_ERR_ARG).
+ *   - out may be q itself when q_stride = n_q_heads * head_dim or for one sequence, and must not
+ *     overlap it otherwise.  out, lse and the workspace must not overlap one another, pages, lens
+ *     or (lse, workspace) q (W4A4_ERR_ARG for all of these), and must not lie in the cache.
  *   - max_pages * page_size is at most 2^30, n_seqs at most 2^24, and n_seqs * n_q_heads *
  *     max_pages * page_size / 16 below 2^31 at the least (W4A4_ERR_SHAPE above).
  *   - A length above max_pages * page_size counts as that many, and a row whose

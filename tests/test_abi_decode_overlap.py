@@ -4,7 +4,7 @@ import ctypes
 
 import pytest
 
-from test_abi_decode import A, ARG, SHAPE, AppendT, CacheT, GroupT, lib  # noqa: F401  (lib: the library as a fixture)
+from test_abi_decode import A, ARG, SHAPE, AppendT, AttendT, CacheT, GroupT, lib  # noqa: F401  (lib: the library as a fixture)
 
 FAR = 1 << 40  # addresses of arrays that take no part
 
@@ -48,8 +48,8 @@ def test_append_to_keys_that_are_the_values(lib):  # noqa: F811
 
 
 def around(bytes_out, bytes_in, step=16):
-    """Every offset at which an output of some bytes meets an input of others, and a few that only touch its ends."""
-    ends = {s * step + o for s in range(2) for o in (-bytes_out + step, bytes_in - 2 * step)}
+    """Aligned offsets at which an output of some bytes still meets an input of others: its ends and about its start."""
+    ends = {s * step + o // step * step for s in range(2) for o in (-bytes_out + step, bytes_in - 2 * step)}
     return sorted({o for o in ends | {0, -step, step} if -bytes_out < o < bytes_in})
 
 
@@ -72,3 +72,26 @@ def test_group_products_over_what_they_read(lib):  # noqa: F811
         assert lib.w4a4_group_pack(FAR, 2 * FAR - at, w, None) == ARG, at
     for at in around(2 * N * K, packed):
         assert lib.w4a4_group_dequantize(w, 2 * FAR + at, None) == ARG, at
+
+
+def test_attend_outputs_over_what_it_reads_and_each_other(lib):  # noqa: F811
+    B, Hq, H, D, max_pages = 3, 4, 2, 64, 5
+    need = lib.w4a4_kv_attend_workspace_bytes(B, Hq, H, D)
+    rows, stride = 2 * B * Hq * D, Hq * D + 8
+    size = dict(out=rows, lse=4 * B * Hq, workspace=need, pages=4 * B * max_pages, lens=4 * B,
+                q=2 * ((B - 1) * stride + Hq * D))
+    place = {n: (6 + i) * FAR for i, n in enumerate(size)}
+
+    def f(**kw):
+        a = dict(place, q_stride=stride, workspace_bytes=need + 4096, n_seqs=B, max_pages=max_pages, n_q_heads=Hq, scale=0.125)
+        a.update(kw)
+        return lib.w4a4_kv_attend(cache(), ctypes.byref(AttendT(**a)), None)
+
+    for written in ("out", "lse", "workspace"):
+        for other in size:
+            if other == written:
+                continue
+            for at in around(size[written], size[other]):
+                gap = other == "q" and any(t * 2 * stride + 2 * Hq * D <= at and at + size[written] <= (t + 1) * 2 * stride
+                                           for t in range(B))
+                assert gap or f(**{written: place[other] + at}) == ARG, (written, other, at)

@@ -1254,6 +1254,24 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
     const int64_t items = static_cast<int64_t>(Hk / a.team) * a.chunks;
     if (items * pieces >= (int64_t(1) << 31) / t.n_seqs) return W4A4_ERR_SHAPE;
   }
+  {  // nothing that is written lies in what is read, nor in another output
+    const size_t rows = static_cast<size_t>(t.n_seqs) * Hq;
+    const struct {
+      const void *at;
+      size_t bytes;
+    } written[3] = {{t.out, 2 * rows * D}, {t.workspace, part_bytes(a.group, D)}, {t.lse, t.lse ? 4 * rows : 0}},
+      read[2] = {{t.pages, 4 * static_cast<size_t>(t.n_seqs) * t.max_pages}, {t.lens, 4 * static_cast<size_t>(t.n_seqs)}};
+    for (int i = 0; i < 3; ++i) {
+      if (!written[i].bytes) continue;
+      for (int j = 0; j < i; ++j)
+        if (overlap_bytes(written[i].at, written[i].bytes, written[j].at, written[j].bytes)) return W4A4_ERR_ARG;
+      for (const auto &r : read)
+        if (r.bytes && overlap_bytes(written[i].at, written[i].bytes, r.at, r.bytes)) return W4A4_ERR_ARG;
+      if (i > 0 && overlap(t.q, t.n_seqs, static_cast<int64_t>(Hq) * D, t.q_stride,
+                           static_cast<const uint16_t *>(written[i].at), (written[i].bytes + 1) / 2))
+        return W4A4_ERR_ARG;
+    }
+  }
   int shift = 0;  // page_size <= 2^shift
   while ((int64_t(1) << shift) < a.cache.page_size) ++shift;
   a.div_shift = 31 + shift;
