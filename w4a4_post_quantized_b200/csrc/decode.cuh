@@ -1,5 +1,9 @@
 // decode.cuh -- shared by the single-token operators (group.cu, kv.cu): the
-// two 16-bit types and the device status.
+// two 16-bit types and checks of arguments.
+//
+// The operators' kernels start while the one in front still writes, so they read with ordinary
+// loads only, behind their wait: non-coherent ones (__ldg, const pointers marked __restrict__)
+// are for memory that nothing writes during a kernel's lifetime.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -80,7 +80,7 @@ __device__ __noinline__ int slow_code(float x, float step) {
 
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_quantize_kernel(const uint16_t *__restrict__ W, GroupShape s, uint8_t *__restrict__ data) {
+    group_quantize_kernel(const uint16_t *W, GroupShape s, uint8_t *data) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;  // groups of a block, words j of a group
   griddep_wait();
   griddep_launch_dependents();
@@ -149,41 +149,45 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 }
 
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_pack_kernel(const uint8_t *__restrict__ codes, const uint16_t *__restrict__ scales, GroupShape s,
-                      uint8_t *__restrict__ data) {
+    group_pack_kernel(const uint8_t *codes, const uint16_t *scales, GroupShape s, uint8_t *data) {
   griddep_wait();
   griddep_launch_dependents();
   Unit u;
   if (!unit_of_warp(s, u)) return;
   const int lane = threadIdx.x & 31, per = kBlockK / s.group;
   uint8_t *record = data + u.at * record_bytes(s.group);
+  const int g = (u.k / kBlockK) * per + (lane & 3), groups = s.K / s.group;  // this lane's group, where it has one
+  uint32_t v[2][4];
+  uint16_t step[2] = {0, 0};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int n = u.row + 8 * h;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[h][j] = 0;
+      if (n < s.N && u.k + 32 * j < s.K)
+        v[h][j] = *reinterpret_cast<const uint32_t *>(codes + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
+    }
+    if ((lane & 3) < per && n < s.N && g < groups) step[h] = scales[static_cast<int64_t>(n) * groups + g];
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
     uint32_t word[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      uint32_t v = 0;
-      if (n < s.N && u.k + 32 * j < s.K)
-        v = *reinterpret_cast<const uint32_t *>(codes + static_cast<int64_t>(n) * (s.K / 2) + (u.k + 32 * j) / 2);
       // nibbles 0, 2, 4, 6 meet in bytes 0 and 2 of one word, 1, 3, 5, 7 in those of another
-      const uint32_t even = v & 0x0F0F0F0Fu, odd = (v >> 4) & 0x0F0F0F0Fu;
+      const uint32_t even = v[h][j] & 0x0F0F0F0Fu, odd = (v[h][j] >> 4) & 0x0F0F0F0Fu;
       word[j] = __byte_perm(even | (even >> 4), odd | (odd >> 4), 0x6420);
     }
-    *reinterpret_cast<uint4 *>(record + 512 * h + 16 * lane) =
-        make_uint4(word[0], word[1], word[2], word[3]);
-    const int g0 = (u.k / kBlockK) * per, groups = s.K / s.group;
-    if ((lane & 3) < per) {
-      const int g = lane & 3;
-      reinterpret_cast<uint16_t *>(record + 1024)[((lane >> 2) * per + g) * 2 + h] =
-          n < s.N && g0 + g < groups ? scales[static_cast<int64_t>(n) * groups + g0 + g] : uint16_t(0);
-    }
+    *reinterpret_cast<uint4 *>(record + 512 * h + 16 * lane) = make_uint4(word[0], word[1], word[2], word[3]);
+    if ((lane & 3) < per)
+      reinterpret_cast<uint16_t *>(record + 1024)[((lane >> 2) * per + (lane & 3)) * 2 + h] = step[h];
   }
 }
 
 template <typename T, int GROUP>
 __global__ void __launch_bounds__(32 * kPackWarps)
-    group_dequantize_kernel(const uint8_t *__restrict__ data, GroupShape s, uint16_t *__restrict__ W) {
+    group_dequantize_kernel(const uint8_t *data, GroupShape s, uint16_t *W) {
   constexpr int kPer = kBlockK / GROUP, kWords = 4 / kPer;
   griddep_wait();
   griddep_launch_dependents();
@@ -315,13 +319,13 @@ __global__ void __launch_bounds__(32 * gemv_warps(RT, NT), 1) group_gemv_kernel(
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = __ldg(reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j));
+        for (int j = 0; j < 4; ++j) x[n][j] = *reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j);
     } else {  // the padding's codes are 0, but what stands behind a token may not be finite
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          x[n][j] = k + 32 * j < s.K ? __ldg(reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j))
+          x[n][j] = k + 32 * j < s.K ? *reinterpret_cast<const uint4 *>(x_row[n] + k + 32 * j)
                                      : make_uint4(0u, 0u, 0u, 0u);
     }
   };

@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(32 * kAttendWarps, NT == 1 ? 3 : 2)
     }
     page = -1;
     if (one || (t >= cr.first && t < cr.end))
-      page = __ldg(a.pages.table + static_cast<int64_t>(cb) * a.pages.max_pages + entry);
+      page = a.pages.table[static_cast<int64_t>(cb) * a.pages.max_pages + entry];
     rest = static_cast<int64_t>(a.heads_of(citem) * a.team + member) * a.cache.stride_head +
            (t - entry * a.cache.page_size) * a.cache.stride_token;
     look_lo = max(cr.first - look_t0, 0);
