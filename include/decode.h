@@ -111,7 +111,7 @@ typedef struct {
     uint16_t *k, *v;
     int64_t n_pages;       /* 0 <= n_pages < 2^31 */
     int32_t page_size;     /* >= 1 */
-    int32_t n_heads;       /* >= 1 */
+    int32_t n_heads;       /* 1 .. 65535, as the numbers of query heads below */
     int32_t head_dim;      /* 64 or 128 */
     uint32_t flags;
     int64_t stride_page, stride_token, stride_head;

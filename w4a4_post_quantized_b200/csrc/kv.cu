@@ -995,10 +995,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) kv_join_kernel(AttendArgs a, 
   }
 }
 
+constexpr int kMaxSeqs = 1 << 24, kMaxHeads = 65535;
+
 w4a4_status check_cache(const w4a4_kv_cache_t *c, Cache *out) {
   if (!c) return W4A4_ERR_ARG;
   if ((c->flags & ~W4A4_FLAG_FP16) || (c->head_dim != 64 && c->head_dim != 128)) return W4A4_ERR_UNSUPPORTED;
-  if (c->n_pages < 0 || c->n_pages >= (int64_t(1) << 31) || c->page_size < 1 || c->n_heads < 1 || c->n_heads > 65535)
+  if (c->n_pages < 0 || c->n_pages >= (int64_t(1) << 31) || c->page_size < 1 || c->n_heads < 1 || c->n_heads > kMaxHeads)
     return W4A4_ERR_SHAPE;
   const int64_t strides[3] = {c->stride_page, c->stride_token, c->stride_head};
   for (int64_t s : strides) {
@@ -1013,7 +1015,7 @@ w4a4_status check_cache(const w4a4_kv_cache_t *c, Cache *out) {
 }
 
 w4a4_status check_pages(const int32_t *pages, int32_t n_seqs, int32_t max_pages) {
-  if (n_seqs < 0 || n_seqs > (1 << 24) || max_pages < 0 || static_cast<int64_t>(n_seqs) * max_pages >= (int64_t(1) << 31))
+  if (n_seqs < 0 || n_seqs > kMaxSeqs || max_pages < 0 || static_cast<int64_t>(n_seqs) * max_pages >= (int64_t(1) << 31))
     return W4A4_ERR_SHAPE;
   if (static_cast<int64_t>(n_seqs) * max_pages > 0 && !pages) return W4A4_ERR_ARG;
   return ptr_aligned4(pages) ? W4A4_OK : W4A4_ERR_ALIGN;
@@ -1147,7 +1149,7 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   if (t.flags & ~W4A4_FLAG_ROPE_PAIRS) return W4A4_ERR_UNSUPPORTED;
   const int D = cache->head_dim, Hk = a.cache.heads, Hq = t.q ? t.n_q_heads : 0;
   if (t.rot_dim < 0 || t.rot_dim > D || t.rot_dim % 16) return W4A4_ERR_UNSUPPORTED;
-  if (t.n_tokens < 0 || t.n_tokens >= (int64_t(1) << 31) || t.n_table < 0 || (t.q && (Hq < 1 || Hq > 65535)))
+  if (t.n_tokens < 0 || t.n_tokens >= (int64_t(1) << 31) || t.n_table < 0 || (t.q && (Hq < 1 || Hq > kMaxHeads)))
     return W4A4_ERR_SHAPE;
   if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
   if ((a.cache.n_pages > 1 && a.cache.stride_page < D) || (a.cache.page_size > 1 && a.cache.stride_token < D) ||
@@ -1205,9 +1207,11 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
 }
 
 size_t w4a4_kv_attend_workspace_bytes(int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim) {
-  if (n_seqs < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
+  using namespace w4a4;
+  if (n_seqs < 0 || n_seqs > kMaxSeqs || n_q_heads < 1 || n_q_heads > kMaxHeads || n_kv_heads < 1 ||
+      n_q_heads % n_kv_heads || (head_dim != 64 && head_dim != 128))
     return 0;
-  return w4a4::part_bytes(n_q_heads / n_kv_heads, head_dim);
+  return part_bytes(n_q_heads / n_kv_heads, head_dim);
 }
 
 w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t *tokens, void *stream) {
@@ -1218,7 +1222,7 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   if (!tokens) return W4A4_ERR_ARG;
   const w4a4_kv_attend_t &t = *tokens;
   const int D = cache->head_dim, Hk = a.cache.heads, Hq = t.n_q_heads;
-  if (Hq < 1 || Hq > 65535 || Hq % Hk || t.window < 0) return W4A4_ERR_SHAPE;
+  if (Hq < 1 || Hq > kMaxHeads || Hq % Hk || t.window < 0) return W4A4_ERR_SHAPE;
   if ((st = check_pages(t.pages, t.n_seqs, t.max_pages)) != W4A4_OK) return st;
   if (static_cast<int64_t>(t.max_pages) * a.cache.page_size > (int64_t(1) << 30)) return W4A4_ERR_SHAPE;
   if (!std::isfinite(t.scale * kLog2e)) return W4A4_ERR_ARG;
