@@ -70,6 +70,20 @@ def test_products_of_random_tokens(w4, M, N, K, group, dt):
     assert torch.all((Y.double().cpu() - want).abs() <= tol)
 
 
+@pytest.mark.parametrize("dt", [BF16, FP16])
+def test_an_infinite_token_makes_every_result_of_its_row_infinite_or_nan(w4, dt):
+    """Each result has the infinity, with the sign of its weight, or NaN where the code is 0; a NaN is in all of them."""
+    N, K, group = 1000, 1024, 32
+    X, codes, steps, want = product_case(6, N, K, group, dt, 9)
+    X[1, 7], X[2, 1000], X[3, 7], X[3, 640], X[4, 100] = math.inf, -math.inf, math.inf, -math.inf, math.nan
+    W = codes.double() * steps.double().repeat_interleave(group, 1)
+    want = torch.stack([(x.double() * W).sum(1) for x in X])
+    Y = w4.w4a4_group_gemv(X.cuda(), w4.w4a4_group_pack(packed_codes(codes).cuda(), steps.cuda())).double().cpu()
+    assert (codes[:, [7, 1000, 640]] == 0).any(0).all() and not Y[1:4].isfinite().any() and Y[4].isnan().all()
+    assert torch.equal(Y.isnan(), want.isnan())
+    assert torch.equal(Y.nan_to_num(0.0, 1e30, -1e30), want.to(dt).double().nan_to_num(0.0, 1e30, -1e30))
+
+
 # --------------------------------------------------------------- attention
 def cache_of(w4, K, V, page, seed, hnd=False):
     """One sequence's keys and values [n, H, D] in shuffled pages; what is left of the last page, and a page more, is NaN."""
