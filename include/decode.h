@@ -186,7 +186,8 @@ typedef struct {
  * head h, which reads cache head h / (n_q_heads / n_heads),
  *   out[b, h] = sum_t p_t V[t],  p = softmax_t(scale * q[b, h] . K[t])
  * over positions t in [max(0, lens[b] - window), lens[b]) (window 0: all).
- * Statistics and sums are fp32, weights two 16-bit terms (2^-16); the result is rounded once.  A sequence
+ * Statistics and sums are fp32; the weights that multiply values are held to 2^-16 of themselves, in fp16 to
+ * 2^-40 of the largest where that is more; the result is rounded once.  A sequence
  * with nothing to attend to (length 0 or negative), or all of whose scores are -inf, gets
  * zeros, and lse = -inf.
  *   - Rows of a page at or behind the length, or in front of the window, are never used,

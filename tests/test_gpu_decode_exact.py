@@ -201,3 +201,31 @@ def test_random_scores_over_long_caches(w4, B, L, H, G, D, dt):
             assert tol.median() < 0.1 * o.abs().median()
             assert torch.all((out[b].double().cpu().view(H, G, D) - o).abs() <= tol)
             assert torch.all((lse[b].double().cpu().view(H, G) - l).abs() <= l_bound)
+
+
+@pytest.mark.parametrize("dt", [BF16, FP16])
+@pytest.mark.parametrize("power", [10, 20, 24, 26, 28, 30])
+@pytest.mark.parametrize("n,D", [(64, 64), (5000, 128), (40_000, 64)])
+def test_weights_far_below_the_largest(w4, n, D, power, dt):
+    """Every 16th token has weight 1 and value 0, the others 2^-power 2/3 and value 2^15: all of the result comes from weights
+    that are held to 2^-16 of themselves or, in fp16, to 2^-40 of the largest, whichever is more (a step of 2^-24 where
+    the largest is 2^15), and that all round the same way."""
+    V = torch.full((n, 1, D), 2.0 ** 15, dtype=dt)
+    K = torch.zeros(n, 1, D, dtype=dt)
+    K[5::16, 0, 0], V[5::16] = 1.0, 0.0
+    cache, pages = cache_of(w4, K, V, 64, power)
+    q = torch.zeros(1, 1, D, dtype=dt)
+    q[..., 0] = float(power)
+    exponent = power + math.log2(1.5)
+    scale = exponent / power * math.log(2.0)
+    tops = len(range(5, n, 16))
+    w = 2.0 ** -exponent
+    want = (n - tops) * w * 2.0 ** 15 / (tops + (n - tops) * w)
+    held = 2.0 ** -16 if dt == BF16 else max(2.0 ** -16, 2.0 ** (exponent - 40))
+    # roundings of scale, scale * log2(e), the score and the difference; the power; sums as in random_scores, 12 pieces
+    rel = held + 4 * exponent * 2.0 ** -24 + 2.0 ** -21 + (12 * (71 + 11) + 2 * (444 + 128)) * 2.0 ** -23
+    h = torch.finfo(dt).eps / 2
+    for out, lse in attend_exact(w4, q, cache, pages, torch.tensor([n], dtype=torch.int32), scale=scale):
+        assert torch.all((out.double().cpu() / want - 1).abs() <= h + (1 + h) * rel)
+        top = exponent * math.log(2.0) + math.log(tops + (n - tops) * w)
+        assert abs(float(lse) - top) <= rel - held + 2.0 ** -22 * (17 + 2 * top)

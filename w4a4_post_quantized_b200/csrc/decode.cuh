@@ -75,8 +75,8 @@ struct Bf16 {
 };
 
 struct Fp16 {
-  // Weights go up to 2^15, so that those down to 2^-39 of the largest are held (2^-24 is the least there is;
-  // 2^-26 of 1 would be lost, and a hundred thousand of those are 2^-9 of the sum).
+  // Weights go up to 2^15, so that those down to 2^-39 of the largest are held, to 2^-40 of it (2^-24 is the
+  // least there is; 2^-26 of 1 would be lost, and a hundred thousand of those are 2^-9 of the sum).
   static constexpr float kTop = 15.0f;
   static __device__ __forceinline__ float to_f32(uint16_t v) { return __half2float(__ushort_as_half(v)); }
   static __device__ __forceinline__ float lo(uint32_t w) { return to_f32(static_cast<uint16_t>(w & 0xFFFFu)); }
