@@ -33,7 +33,7 @@ struct AppendArgs {
   const uint16_t *k, *v, *q;
   uint16_t *q_out;
   int64_t k_stride, v_stride, q_stride;
-  int q_heads, head_dim, rot_dim, n_table;
+  int q_heads, rot_dim, n_table;
   const int32_t *seq, *pos, *table_pos;
   const float *table;
   bool pairs;
@@ -1182,7 +1182,6 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   a.v_stride = t.v_stride;
   a.q_stride = t.q_stride;
   a.q_heads = Hq;
-  a.head_dim = D;
   a.rot_dim = t.rot_dim;
   a.n_table = t.n_table;
   a.seq = t.seq;
