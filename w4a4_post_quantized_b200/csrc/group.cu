@@ -35,7 +35,8 @@ __host__ __device__ constexpr int record_bytes(int group) { return 1024 + 32 * (
 // warp's 512 in a row), a group's maximum needs two exchanges between four
 // lanes, and all eight 16-byte loads are in flight at once.  (One thread per 8
 // inputs, with the rows' order on both sides: 20000 x 8192 there and back took 411
-// us; now 65 and 64, 99 % of a copy's rate.)
+// us; now 65 and 64, 99 % of a copy's rate.  Packing, whose loads are 4 bytes, all asked for before the
+// first store: 47.4 us at 32768 x 8192, 90 %.)
 
 constexpr int kPackWarps = 8;
 
@@ -246,13 +247,18 @@ __global__ void __launch_bounds__(32 * kPackWarps)
 //    other, 8 tokens: 5.5 us instead of 5.6 at 2048 x 8192, 7.3 instead of 7.5 at 8192 x
 //    4096; the smallest lose 0.1.)
 //
-// 32768 x 8192, groups of 128: 1 token 30.3 us, 8 31.0 (4.5 TB/s, 70 % of a copy), 16 45.5.
-// Large shapes are bound by the instructions that widen codes: issue slots 63 %, the
-// integer and logic pipe 59 % busy, the tensor pipe 26 %.  The same kernel with codes
-// used as they are takes 26.2, without its products 24.2.
+// 32768 x 8192, groups of 128, no bias: 1 token 29.2 us, 8 29.6 (4.7 TB/s, 72 % of a copy), 16 41.5.
+// At 8 tokens (30.7 with a bias) no single thing is full: issue slots 64 %, the integer and
+// logic pipe 60 %, the tensor pipe 26 %.  Widening the codes is 5 us of it (26.2 with codes used as
+// they are), the products 2 more (24.2 without).  16 tokens take as many instructions (20.8
+// million warp instructions, 20.7 with 8), but from half the warps, two to a scheduler, at 46 %
+// of the issue slots: a warp waits for its own results (1.3 cycles an issue for dependences, 0.6
+// for the tensor pipe, 38 % busy, 0.4 for tokens) and there is too little else to issue.
 
 // Warps of a block: 16 tiles of two sets of columns need twice the registers, and their sums
-// would not fit into shared memory 16 times.
+// would not fit into shared memory 16 times.  16 warps have 128 registers a thread, which does not
+// hold everything: per thread, 8 tiles of two sets spill 140 to 236 bytes, 4 tiles of two sets up to 40, 16
+// tiles of one set 12 to 52, 8 of one set up to 12 in groups of 32; 16 tiles of two sets, with 8 warps, up to 16.
 constexpr int gemv_warps(int RT, int NT) { return RT * NT > 16 ? 8 : 16; }
 // Tiles that a warp takes in one go: two, whose products do not depend on one another and
 // which share the waiting and counting, unless there is only one.
@@ -554,8 +560,9 @@ w4a4_status launch_gemv_t(GemvArgs a, void *stream) {
 
 template <typename T, int GROUP>
 w4a4_status launch_gemv(const GemvArgs &a, void *stream) {
-  // As many tiles at a time as a block has, in steps, up to what its registers hold; fewer at a time
-  // leave the ring more stages (us at N x K on 148 SMs, 8 or 16 tokens):
+  // As many tiles at a time as a block has, in steps: what is not used costs instructions, and with two
+  // sets of columns spilled registers; a single tile is taken alone, with 4 stages of its ring
+  // instead of 2 pairs (us at N x K on 148 SMs, 8 or 16 tokens):
   //   1 tile: alone 5.6 and 6.4, as 4 with three empty 6.7 and 8.1 (2048 x 8192)
   //   2 to 4: up to 8 tokens 8 at a time are as good as 4 (7.2 both, 8192 x 4096); 16 tokens, 4 at a time 9.3, 8 10.7
   //   5 to 8: 8 at a time 11.0 and 16.5, 16 11.6 and 17.4 (16384 x 4096)
