@@ -81,7 +81,7 @@ __device__ __forceinline__ void load4(const float *from, float (&to)[8], int fir
 // neighbouring lanes are neighbours in memory: with each lane's two pieces side by side
 // every sector was written in two halves, 24.6 us instead of 22 for 5003 tokens of 128
 // dims turned in part.  (One block per token, thread by thread over its elements, took 67
-// us for 8 frames; now 25.0, 5.5 TB/s, and 78.6, 98 % of a copy's rate, on 40000 tokens.)
+// us for 8 frames; now 25.0, 5.5 TB/s, and 77.8, 100 % of a copy's rate, on 40000 tokens.)
 constexpr int kAppendWarps = 2;
 
 // Passes of a round.  More are more loads in flight per warp, fewer leave registers for more
@@ -218,8 +218,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
 //    The total adds the weights as they were before.
 //
 // us, and the share of a copy's rate: 64 frames of one sequence (87936 tokens, 16 heads of 64)
-// 57.4, 97 %; 64 sequences of 8192 127, 98 %; 23 of 1 to 4001 37.5, 78 %, where the wait for
-// the first lengths, pages and rows and the join are what is left; one frame (1374 tokens) 7.2,
+// 57.8, 97 %; 64 sequences of 4160 to 8192 126, 99 %; 23 of 250 to 4001 and none 37.5, 78 %, where the
+// wait for the first lengths, pages and rows and the join are what is left; one frame (1374 tokens) 7.2,
 // all of it such waits.  In long ones issue slots are 34 %, the tensor pipe 21 % busy.
 
 constexpr int kAttendWarps = 4;
@@ -1079,7 +1079,8 @@ w4a4_status launch_attend(AttendArgs &a, void *stream) {
   {
     // Clusters of as many blocks for an item as fit on the GPU and have a piece for every warp, where
     // no warp gets many, as far as the host knows: 4; 1 where few items leave most of the GPU to
-    // a finer cut; 12 where blocks of long rows fill half of it.  us with clusters and with the
+    // a finer cut; 12 where blocks of long rows fill half of it.  (The host knows the table's width
+    // only: short sequences under a wide table take the line.)  us with clusters and with the
     // line: 16 heads of 64, 1 sequence of 128 4.1 and 5.6, 1 of 1374 7.2 and 7.6, 16 of 500 11.6 and 14.1,
     // of 1374 (11 pieces a warp) 25.1 and 22.9; 8 heads of 128: 1 of 500 5.3 and 6.2, 1 of 4096 (8) 12.1 and
     // 11.2, 16 of 1374 (11, half the GPU) 20.6 and 23.1; 1 head of 64 for 8, 1 of 1374 7.4 and 6.8, 8 of 4096
@@ -1193,8 +1194,8 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
   if (status_word(&status) != cudaSuccess) return W4A4_ERR_CUDA;
   cudaLaunchAttribute attr;
   // shares of a token's heads, at most one per round of a warp, up to about the 24 warps per SM that
-  // fit: 600 tokens of 128 dims and 48 heads 4.9 us (up to 16 warps 5.5, 4 8.9), 1000 6.4 (6.6, 9.2);
-  // 5003 19.4 undivided, 25.0 in as many shares as there are rounds
+  // fit (over the same outputs again): 600 tokens of 128 dims and 48 heads 4.9 us (up to 16 warps 5.5, 4 8.9), 1000
+  // 6.4 (6.6, 9.2); 5003 19.4 undivided, 25.0 in as many shares as there are rounds
   const int round = append_round(D) * (32 / (D / 16)), most = (2 * Hk + Hq + round - 1) / round;
   const int64_t want = (24ll * device_sm_count() + t.n_tokens - 1) / t.n_tokens;
   const int parts = static_cast<int>(want < most ? want : most);
@@ -1246,7 +1247,7 @@ w4a4_status w4a4_kv_attend(const w4a4_kv_cache_t *cache, const w4a4_kv_attend_t 
   // Neighbouring cache heads in a team, except where rows are long and there is little to do
   // for each warp (as far as the host knows): then shares of single heads, whose parts a
   // block joins by itself, win.  us with teams and without, 8 heads of 128: 1 sequence of 1024
-  // tokens 7.8 and 7.1, 23 of up to 4001 38.4 and 37.6; 64 of 2048 83.9 and 87.5, 16 of 16384
+  // tokens (in L2) 7.8 and 7.1, 23 of up to 4001 38.4 and 37.6; 64 of 2048 83.9 and 87.5, 16 of 16384
   // 158.2 and 160.5.  Of 64 (16 heads, 64 of 2048, by token): 87.7 and 94.5.
   const int64_t warps = 3 * kAttendWarps * device_sm_count();
   if (D == 64 || (room / 16) * Hk * a.chunks >= 32 * warps / t.n_seqs)
