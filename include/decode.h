@@ -146,8 +146,8 @@ typedef struct {
 /* New tokens enter the cache: token t with keys k[t] and values v[t] becomes position pos[t]
  * of sequence seq[t], which lives in page pages[seq, pos / page_size] at row pos %
  * page_size.  Keys, and queries on their way from q to q_out (which may be q itself when
- * q_stride = n_q_heads * head_dim or for one token, and must not overlap it otherwise, nor k or v:
- * W4A4_ERR_ARG), are rotated: with
+ * q_stride = n_q_heads * head_dim or for one token, and must not overlap it otherwise, nor any
+ * other array that is read: W4A4_ERR_ARG), are rotated: with
  * (a, b) elements i and i + rot_dim / 2 (W4A4_FLAG_ROPE_PAIRS: 2i and 2i + 1) of a head and
  * (c, s) elements i and i + rot_dim / 2 of the token's row of the table, a' = a c - b s, b' =
  * b c + a s in fp32, rounded once; elements from rot_dim on, values, and everything when

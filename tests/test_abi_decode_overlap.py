@@ -95,3 +95,15 @@ def test_attend_outputs_over_what_it_reads_and_each_other(lib):  # noqa: F811
                 gap = other == "q" and any(t * 2 * stride + 2 * Hq * D <= at and at + size[written] <= (t + 1) * 2 * stride
                                            for t in range(B))
                 assert gap or f(**{written: place[other] + at}) == ARG, (written, other, at)
+
+
+def test_append_queries_over_what_is_looked_up(lib):  # noqa: F811
+    """Pages, positions, sequences and the rotation's table are read by every warp of a token, whenever it comes."""
+    T, Hq, n_seqs, max_pages, n_table, rot = 8, 2, 6, 2, 5, 16
+    size = dict(pages=4 * n_seqs * max_pages, pos=4 * T, seq=4 * T, table_pos=4 * T, table=4 * n_table * rot)
+    place = {n: (6 + i) * FAR for i, n in enumerate(size)}
+    for name, n in size.items():
+        for at in around(2 * T * Hq * 64, n):
+            a = dict(place, k=FAR, v=2 * FAR, q=3 * FAR, q_out=place[name] + at, k_stride=256, v_stride=256, q_stride=128, n_tokens=T,
+                     n_seqs=n_seqs, max_pages=max_pages, n_q_heads=Hq, n_table=n_table, rot_dim=rot)
+            assert lib.w4a4_kv_append(cache(), ctypes.byref(AppendT(**a)), None) == ARG, (name, at)

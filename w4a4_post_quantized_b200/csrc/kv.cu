@@ -1173,6 +1173,15 @@ w4a4_status w4a4_kv_append(const w4a4_kv_cache_t *cache, const w4a4_kv_append_t 
         overlap(t.k, t.n_tokens, kv_row, t.k_stride, t.q_out, t.n_tokens * q_row) ||
         overlap(t.v, t.n_tokens, kv_row, t.v_stride, t.q_out, t.n_tokens * q_row))
       return W4A4_ERR_ARG;
+    const size_t per_token = 4 * static_cast<size_t>(t.n_tokens);
+    const struct {
+      const void *at;
+      size_t bytes;
+    } read[5] = {{t.pages, 4 * static_cast<size_t>(t.n_seqs) * t.max_pages}, {t.pos, per_token}, {t.seq, per_token},
+                 {t.table_pos, per_token}, {t.table, 4 * static_cast<size_t>(t.n_table) * t.rot_dim}};
+    for (const auto &r : read)
+      if (r.at && r.bytes && overlap_bytes(t.q_out, 2 * static_cast<size_t>(t.n_tokens) * q_row, r.at, r.bytes))
+        return W4A4_ERR_ARG;
   }
   a.pages = {t.pages, t.n_seqs, t.max_pages};
   a.k = t.k;
